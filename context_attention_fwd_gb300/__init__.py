@@ -12,9 +12,12 @@ library how they are stored.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 import threading
+from dataclasses import dataclass
 
 import torch
 
@@ -24,6 +27,7 @@ __all__ = [
     "attn_fwd", "attn_bwd", "seq_head_exchange", "exchanged_view", "workspace_size",
     "chunk_offsets", "device_status", "selftest_wait_timeout", "library_path", "load_library",
     "profile_enable", "profile_read", "launch_plan", "debug_set", "kernel_binary_version",
+    "RopeTable", "rope_table", "rope_fwd", "rope_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
     "CtxError", "FLAG_MATERIALIZE_PARTIALS", "FLAG_KV_ALLGATHER", "DEBUG_SKIP_ARRIVAL",
 ]
 
@@ -46,6 +50,13 @@ class _Tensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("B", ctypes.c_int64), ("S", ctypes.c_int64),
                 ("H", ctypes.c_int64), ("D", ctypes.c_int64), ("stride_b", ctypes.c_int64),
                 ("stride_s", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("n_axes", ctypes.c_int), ("sections", ctypes.c_int * 4), ("magnitude", ctypes.c_float),
+                ("positions", ctypes.c_void_p), ("pos_stride_b", ctypes.c_int64), ("pos_stride_s", ctypes.c_int64),
+                ("pos_stride_axis", ctypes.c_int64), ("offset", ctypes.c_int64)]
 
 
 class _Plan(ctypes.Structure):
@@ -86,12 +97,20 @@ def load_library(build_if_missing: bool = True):
             lib.ctx_attn_launch_plan.argtypes = [I, I, I, I, I, I, P(I), I, P(_Plan)]
             lib.ctx_debug_set.argtypes = [ctypes.c_uint, ctypes.c_uint]
             lib.ctx_kernel_binary_version.argtypes = [P(I)]
+            R = P(_Rope)
+            lib.ctx_rope_fwd.argtypes = [T, T, R, I, I, T, T, V]
+            lib.ctx_rope_bwd.argtypes = [T, T, R, I, I, T, T, V]
+            lib.ctx_qk_norm_rope_fwd.argtypes = [T, T, V, V, I, F, R, I, I, T, T, V]
+            lib.ctx_qk_norm_rope_bwd.argtypes = [T, T, T, T, V, V, I, F, R, I, I, T, T, V, V, V, SZ, V]
+            lib.ctx_qk_norm_rope_workspace_size.argtypes = [I]
+            lib.ctx_qk_norm_rope_workspace_size.restype = SZ
             lib.ctx_status_string.argtypes = [I]
             lib.ctx_status_string.restype = ctypes.c_char_p
             for n in ("ctx_attn_fwd", "ctx_attn_bwd", "ctx_seq_head_exchange", "ctx_chunk_offsets",
                       "ctx_get_device_status", "ctx_selftest_wait_timeout", "ctx_profile_enable",
                       "ctx_profile_read", "ctx_selftest_exp2", "ctx_attn_launch_plan", "ctx_debug_set",
-                      "ctx_kernel_binary_version"):
+                      "ctx_kernel_binary_version", "ctx_rope_fwd", "ctx_rope_bwd", "ctx_qk_norm_rope_fwd",
+                      "ctx_qk_norm_rope_bwd"):
                 getattr(lib, n).restype = I
             _lib = lib
     return _lib
@@ -294,6 +313,256 @@ def exchanged_view(y, S, layout):
         raise ValueError("the batched view exists for [B,S,H,D] storage; use y[u] per group")
     U, B, Sp, Hu, D = y.shape
     return y.view(U * B, Sp, Hu, D)[:, :S]
+
+
+# ---------------------------------------------------------------- rotary positions, query/key norms
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _on(device):
+    """Makes `device` current for a launch when it is not."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+@dataclass(frozen=True)
+class RopeTable:
+    """Frequencies of a rotary embedding, laid out once (``rope_table``)."""
+    turns: torch.Tensor  # int64 [rot_dim / 2]: turns per position as a fraction of 2^64
+    rot_dim: int
+    interleaved: bool
+    sections: tuple      # pairs per position axis
+    magnitude: float
+
+
+def rope_table(rot_dim, theta=10000.0, interleaved=False, sections=None, scaling="none", factor=1.0,
+               original_len=None, beta_fast=32.0, beta_slow=1.0, magnitude=None, inv_freq=None,
+               device=None) -> RopeTable:
+    """The frequency table that the rotary calls take.
+
+    Pair i of the first ``rot_dim`` elements turns by theta^(-2 i / rot_dim)
+    radians per position.  ``interleaved``: pairs are neighbours (2 i, 2 i + 1)
+    instead of (i, i + rot_dim / 2).  ``sections`` gives every position axis
+    its own run of pairs with its own frequencies, theta^(-2 i / (2 n)) for a
+    section of n pairs; positions then carry one value per axis.
+
+    ``scaling`` stretches the context by ``factor``: "linear" divides every
+    frequency by it; "ntk" raises theta to theta * factor^(d / (d - 2));
+    "yarn" (Peng et al. 2023, "YaRN: Efficient Context Window Extension of
+    Large Language Models") divides by it the frequencies that turn less than
+    ``beta_slow`` times over ``original_len`` positions, keeps those that turn
+    more than ``beta_fast`` times, blends linearly between, and multiplies the
+    rotated part by 0.1 ln(factor) + 1.  ``magnitude`` overrides that
+    multiplier; ``inv_freq`` (radians per position, one per pair) overrides
+    the frequencies."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim: expected an even number >= 2, got {rot_dim}")
+    secs = (rot_dim // 2,) if sections is None else tuple(int(n) for n in sections)
+    if not 1 <= len(secs) <= 4 or min(secs) < 1 or sum(secs) != rot_dim // 2:
+        raise ValueError(f"sections: 1 to 4 positive counts that sum to rot_dim / 2 = {rot_dim // 2}, got {secs}")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling: {scaling!r} is none of 'none', 'linear', 'ntk', 'yarn'")
+    if not (theta > 1.0 and math.isfinite(theta)) or not (factor >= 1.0 and math.isfinite(factor)):
+        raise ValueError(f"theta must exceed 1 and factor be at least 1, got {theta}, {factor}")
+    if scaling == "yarn" and not original_len:
+        raise ValueError("scaling='yarn' needs original_len")
+    if inv_freq is not None:
+        freq = [float(w) for w in inv_freq]
+        if len(freq) != rot_dim // 2:
+            raise ValueError(f"inv_freq: expected {rot_dim // 2} values, got {len(freq)}")
+    else:
+        freq = []
+        for n in secs:
+            d, base = 2 * n, float(theta)
+            if scaling == "ntk":
+                if d <= 2:
+                    raise ValueError("scaling='ntk' needs sections of more than one pair")
+                base *= factor ** (d / (d - 2.0))
+            w = [base ** (-2.0 * i / d) for i in range(n)]
+            if scaling == "linear":
+                w = [x / factor for x in w]
+            elif scaling == "yarn":
+                pair = lambda turns: d * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+                lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), d - 1)
+                for i in range(n):
+                    slow = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)
+                    w[i] = w[i] / factor * slow + w[i] * (1.0 - slow)
+            freq += w
+    if any(not 0.0 <= w < 2 * math.pi for w in freq):
+        raise ValueError("frequencies must lie in [0, 2 pi) radians per position")
+    if magnitude is None:
+        magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1.0 else 1.0
+    fixed = [int(w / (2 * math.pi) * 2.0 ** 64) for w in freq]
+    turns = torch.tensor([t - (1 << 64) if t >= 1 << 63 else t for t in fixed], dtype=torch.int64)
+    return RopeTable(turns.to("cuda" if device is None else device), int(rot_dim), bool(interleaved), secs,
+                     float(magnitude))
+
+
+def _rope_desc(table, positions, offset, B, S, device):
+    if table is None:
+        if positions is not None:
+            raise ValueError("positions given without a table")
+        return None
+    if table.turns.device != device:
+        raise ValueError(f"table: on {table.turns.device}, the tensors are on {device}")
+    r = _Rope(table.turns.data_ptr(), table.rot_dim, int(table.interleaved), len(table.sections),
+              (ctypes.c_int * 4)(*table.sections), table.magnitude, None, 0, 0, 0, int(offset))
+    if positions is None:
+        if len(table.sections) > 1:
+            raise ValueError("a table with several position axes needs positions")
+        return r
+    if positions.dtype != torch.int64 or positions.device != device:
+        raise ValueError(f"positions: expected int64 on {device}, got {positions.dtype} on {positions.device}")
+    p = positions
+    if len(table.sections) > 1:
+        if p.dim() < 2 or p.shape[-1] != len(table.sections):
+            raise ValueError(f"positions: expected [S, {len(table.sections)}] or [B, S, {len(table.sections)}], "
+                             f"got {tuple(p.shape)}")
+        r.pos_stride_axis = p.stride(-1)
+        p = p.select(-1, 0)
+    if p.dim() == 1 and p.shape[0] == S:
+        r.pos_stride_s = p.stride(0)
+    elif p.dim() == 2 and p.shape[0] in (1, B) and p.shape[1] == S:
+        r.pos_stride_b, r.pos_stride_s = (0 if p.shape[0] == 1 else p.stride(0)), p.stride(1)
+    else:
+        raise ValueError(f"positions: {tuple(positions.shape)} does not fit {B} sequences of {S} tokens")
+    r.positions = positions.data_ptr()
+    return r
+
+
+def _any_desc(t, name):
+    B, S, H, D = t.shape
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the D dimension must be contiguous")
+    return _Tensor(t.data_ptr(), B, S, H, D, t.stride(0), t.stride(1), t.stride(2))
+
+
+def _check_rows(named):
+    """Tensors of one rotary / norm call: ranks, one element type, one device,
+    and the shapes of each side (q's, then k's)."""
+    first = named[0][1]
+    for name, t in named:
+        if t.dim() != 4:
+            raise ValueError(f"{name}: expected a logical [B,S,H,D] tensor, got {t.dim()} dims")
+        if t.dtype not in _DTYPES or t.dtype != first.dtype:
+            raise ValueError(f"{name}: dtype must be bfloat16, float16 or float32, the same for all; got {t.dtype}")
+        if not t.is_cuda or t.device != first.device:
+            raise ValueError(f"{name}: on {t.device}; every tensor must be on one CUDA device")
+        if (t.shape[0], t.shape[1], t.shape[3]) != (first.shape[0], first.shape[1], first.shape[3]):
+            raise ValueError(f"{name}: shape {tuple(t.shape)} does not go with {tuple(first.shape)}")
+
+
+def _rows_like(t):
+    B, S, H, D = t.shape
+    if t.stride(0) >= t.stride(1):
+        return torch.empty(B, S, H, D, dtype=t.dtype, device=t.device)
+    return torch.empty(S, B, H, D, dtype=t.dtype, device=t.device).permute(1, 0, 2, 3)
+
+
+def _ref(t, name):
+    return None if t is None else ctypes.byref(_any_desc(t, name))
+
+
+def _ptr(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _given(*named):
+    return [(n, t) for n, t in named if t is not None]
+
+
+def _rotate(entry, names, a, b, table, positions, offset, a_out, b_out):
+    lib = load_library()
+    if table is None:
+        raise ValueError("table: a RopeTable is required")
+    _check_rows(_given((names[0], a), (names[1], b), (names[2], a_out), (names[3], b_out)))
+    rope = _rope_desc(table, positions, offset, a.shape[0], a.shape[1], a.device)
+    a_out = _rows_like(a) if a_out is None else a_out
+    b_out = _rows_like(b) if b_out is None and b is not None else b_out
+    with _on(a.device):
+        rc = getattr(lib, entry)(_ref(a, names[0]), _ref(b, names[1]), ctypes.byref(rope), _DTYPES[a.dtype],
+                                 LAYOUT_BSHD, _ref(a_out, names[2]), _ref(b_out, names[3]), _stream(a))
+    _check(rc, entry)
+    return a_out, b_out
+
+
+def rope_fwd(q, k, table, positions=None, offset=0, q_out=None, k_out=None):
+    """Rotary positions -> (q_out, k_out), stored like q and k (k may be None).
+
+    q [B,S,Hq,D], k [B,S,Hk,D]: bf16, fp16 or fp32.  ``positions``: int64 [S]
+    or [B,S] ([S,axes] or [B,S,axes] for a table with several axes); without
+    it token s of every sequence is at ``offset + s``.  q_out / k_out may be
+    q / k."""
+    return _rotate("ctx_rope_fwd", ("q", "k", "q_out", "k_out"), q, k, table, positions, offset, q_out, k_out)
+
+
+def rope_bwd(dq_out, dk_out, table, positions=None, offset=0, dq=None, dk=None):
+    """Gradients through ``rope_fwd`` -> (dq, dk): the transposed rotation."""
+    return _rotate("ctx_rope_bwd", ("dq_out", "dk_out", "dq", "dk"), dq_out, dk_out, table, positions, offset, dq, dk)
+
+
+def _check_weights(named, D, device):
+    dt = None
+    for name, w in named:
+        if tuple(w.shape) != (D,) or not w.is_contiguous() or w.device != device or w.dtype not in _DTYPES:
+            raise ValueError(f"{name}: expected a contiguous [{D}] tensor on {device}, got {w.dtype} {tuple(w.shape)}")
+        if dt is not None and w.dtype != dt:
+            raise ValueError(f"{name}: both weights must have one dtype")
+        dt = w.dtype
+    return _DTYPES[dt] if dt is not None else 2
+
+
+def qk_norm_rope_fwd(q, k, wq, wk, table, positions=None, offset=0, eps=1e-6, q_out=None, k_out=None):
+    """Per-head RMS norm of q and k, times their weights, then the rotation, in
+    one pass -> (q_out, k_out).
+
+    wq, wk: [D] weights or None (ones); table None: the norm alone; the other
+    arguments as in ``rope_fwd``."""
+    lib = load_library()
+    _check_rows(_given(("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)))
+    wt = _check_weights(_given(("wq", wq), ("wk", wk)), q.shape[3], q.device)
+    rope = _rope_desc(table, positions, offset, q.shape[0], q.shape[1], q.device)
+    q_out = _rows_like(q) if q_out is None else q_out
+    k_out = _rows_like(k) if k_out is None and k is not None else k_out
+    with _on(q.device):
+        rc = lib.ctx_qk_norm_rope_fwd(_ref(q, "q"), _ref(k, "k"), _ptr(wq), _ptr(wk), wt, float(eps),
+                                      None if rope is None else ctypes.byref(rope), _DTYPES[q.dtype], LAYOUT_BSHD,
+                                      _ref(q_out, "q_out"), _ref(k_out, "k_out"), _stream(q))
+    _check(rc, "ctx_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, table, positions=None, offset=0, eps=1e-6, dq=None, dk=None,
+                     dwq=None, dwk=None, workspace=None):
+    """Gradients through ``qk_norm_rope_fwd`` -> (dq, dk, dwq, dwk).
+
+    q, k are the forward's inputs; nothing else is saved.  dwq, dwk: fp32 [D]
+    (None for a weight that is None), summed in a fixed order."""
+    lib = load_library()
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out go together")
+    _check_rows(_given(("q", q), ("dq_out", dq_out), ("k", k), ("dk_out", dk_out), ("dq", dq), ("dk", dk)))
+    D, dev = q.shape[3], q.device
+    wt = _check_weights(_given(("wq", wq), ("wk", wk)), D, dev)
+    for name, g, w in (("dwq", dwq, wq), ("dwk", dwk, wk)):
+        if g is not None and (w is None or g.dtype != torch.float32 or tuple(g.shape) != (D,)
+                              or not g.is_contiguous() or g.device != dev):
+            raise ValueError(f"{name}: expected a contiguous float32 [{D}] tensor on {dev}, beside its weight")
+    rope = _rope_desc(table, positions, offset, q.shape[0], q.shape[1], dev)
+    dq = _rows_like(q) if dq is None else dq
+    dk = _rows_like(k) if dk is None and k is not None else dk
+    dwq = torch.empty(D, dtype=torch.float32, device=dev) if dwq is None and wq is not None else dwq
+    dwk = torch.empty(D, dtype=torch.float32, device=dev) if dwk is None and wk is not None else dwk
+    need = lib.ctx_qk_norm_rope_workspace_size(D) if dwq is not None or dwk is not None else 0
+    ws, wsb = _workspace(need, dev, workspace)
+    with _on(dev):
+        rc = lib.ctx_qk_norm_rope_bwd(_ref(dq_out, "dq_out"), _ref(dk_out, "dk_out"), _ref(q, "q"), _ref(k, "k"),
+                                      _ptr(wq), _ptr(wk), wt, float(eps), None if rope is None else ctypes.byref(rope),
+                                      _DTYPES[q.dtype], LAYOUT_BSHD, _ref(dq, "dq"), _ref(dk, "dk"), _ptr(dwq),
+                                      _ptr(dwk), _ptr(ws), wsb, _stream(q))
+    _check(rc, "ctx_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
 
 
 def device_status(stream=None) -> int:

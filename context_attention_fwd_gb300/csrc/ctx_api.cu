@@ -13,9 +13,7 @@
 #include <mutex>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
-#include "../../include/ctx_attn.h"
+#include "api_util.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -60,30 +58,6 @@ int kernel_debug_bits() {
     return (g_debug_flags.load(std::memory_order_relaxed) & CTX_DEBUG_SKIP_ARRIVAL) ? kDebugSkipArrival : 0;
 }
 
-// CTX_ATTN_LOG=1: one line per attention call on stderr (schedule, tiles,
-// kernel variant).
-bool log_enabled() {
-    static const bool on = [] {
-        const char* e = getenv("CTX_ATTN_LOG");
-        return e && *e && *e != '0';
-    }();
-    return on;
-}
-
-// An NVTX range around an entry point (visible in a profiler's timeline;
-// nearly free when no tool is attached).
-struct NvtxRange {
-    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-};
-
-int num_sms() {
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n > 0 ? n : 148;
-}
-
 // Launch order of the attention kernels.  Under causal masking the work of
 // a CTA falls off along the tile index, and the kernels launch the heaviest
 // tile of a head first.  On grids of a few waves the order across heads
@@ -115,39 +89,6 @@ int use_pdl(int64_t ctas, int ntiles, cudaStream_t s) {
     return st == cudaStreamCaptureStatusNone ? 1 : 0;
 }
 
-struct Dense {
-    void* data;
-    int64_t sb, ss, sh;
-};
-
-// Validates a logical [B,S,H,D] tensor and resolves its strides.
-int resolve(const ctx_tensor_t* t, int64_t B, int64_t S, int64_t H, int64_t D, ctx_layout_t layout,
-            Dense* out) {
-    if (!t || !t->data) return CTX_ERR_INVALID_ARG;
-    if (t->B != B || t->S != S || t->H != H || t->D != D) return CTX_ERR_INVALID_ARG;
-    int64_t sb = t->stride_b, ss = t->stride_s, sh = t->stride_h;
-    if (sb == 0 && ss == 0 && sh == 0) {
-        if (layout == CTX_LAYOUT_BSHD) {
-            sh = D; ss = H * D; sb = S * H * D;
-        } else if (layout == CTX_LAYOUT_SBHD) {
-            sh = D; sb = H * D; ss = B * H * D;
-        } else {
-            return CTX_ERR_INVALID_ARG;
-        }
-    }
-    if (sb < 0 || ss < 0 || sh < 0) return CTX_ERR_INVALID_ARG;
-    if ((B > 1 && sb == 0) || (S > 1 && ss == 0) || (H > 1 && sh == 0)) return CTX_ERR_INVALID_ARG;
-    if (sh < D && H > 1) return CTX_ERR_INVALID_ARG;  // heads would overlap
-    // TMA and 16-byte vector access: 16-byte aligned base and strides
-    if ((reinterpret_cast<uintptr_t>(t->data) & 15) || (sb & 7) || (ss & 7) || (sh & 7))
-        return CTX_ERR_UNSUPPORTED;
-    out->data = t->data;
-    out->sb = sb;
-    out->ss = ss;
-    out->sh = sh;
-    return CTX_OK;
-}
-
 int build_chunks(int S, int P, const int* offsets, ChunkTable* ct) {
     if (P < 1 || P > kMaxChunks || P > S) return CTX_ERR_INVALID_ARG;
     ct->P = P;
@@ -172,8 +113,6 @@ int build_chunks(int S, int P, const int* offsets, ChunkTable* ct) {
     for (int c = P + 1; c <= kMaxChunks; ++c) ct->off[c] = ct->tile_off[c] = ct->pair_off[c] = 0;
     return CTX_OK;
 }
-
-inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 int64_t ntiles_upper(int S, int P) {  // tiles of any chunking of S into P chunks
     return (S + kTile - 1) / kTile + P;
@@ -444,10 +383,6 @@ void prof_record(int kernel, int which, cudaStream_t s) {
     }
     cudaEventRecord(g_prof.ev[kernel][i][which], s);
     if (which == 1) g_prof.n[kernel] = i + 1;
-}
-
-inline int launch_status(cudaError_t launch = cudaSuccess) {
-    return launch == cudaSuccess && cudaGetLastError() == cudaSuccess ? CTX_OK : CTX_ERR_CUDA;
 }
 
 size_t fwd_ws_bytes(int B, int S, int Hq, int D, int P, int flags) {

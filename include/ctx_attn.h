@@ -210,6 +210,73 @@ int64_t ctx_exchange_padded_len(int64_t S, int ring, int ulysses);
 int ctx_seq_head_exchange(const ctx_tensor_t* x, void* y, int ring, int ulysses, int dir,
                           ctx_layout_t layout, ctx_stream_t stream);
 
+/* ---- Rotary positions, and per-head norms of queries and keys ------------
+ *
+ * The steps that stand between a model's projections and its attention call.
+ * They take logical [B,S,H,D] tensors as the attention does, but of any of
+ * three element types, any even D up to 512 and any strides whose D stride is
+ * 1 (rows on 16-byte boundaries with D and rot_dim multiples of 16 take the
+ * wide-access kernels; anything else is right, and slower).  q and k may have
+ * different head counts; k (with its result) may be NULL.  A result may be
+ * its own input (same data and strides); it must not overlap it otherwise. */
+typedef enum { CTX_DTYPE_BF16 = 0, CTX_DTYPE_FP16 = 1, CTX_DTYPE_FP32 = 2 } ctx_dtype_t;
+
+/* Rotary positions.  Pair i (0 <= i < rot_dim / 2) of a head at position p
+ * turns by a = 2 pi p t_i:  (x1, x2) -> magnitude * (x1 cos a - x2 sin a,
+ * x2 cos a + x1 sin a).  The pair is elements (i, i + rot_dim / 2) when
+ * interleaved is 0 and (2 i, 2 i + 1) otherwise; elements from rot_dim on are
+ * not rotated (nor scaled by magnitude). */
+typedef struct {
+    /* Device array [rot_dim / 2]: t_i, the pair's frequency in turns per
+     * position, as a fraction of 2^64 (t_i < 1).  Angles are p * t_i modulo
+     * 2^64, exactly, so they stay accurate at any position. */
+    const uint64_t* turns;
+    int rot_dim;     /* 2 <= rot_dim <= D, even */
+    int interleaved;
+    /* Position axes: with n_axes = 1 every pair uses one position per token;
+     * with 2 to 4 the pairs are split in order, sections[a] of them on axis a
+     * (their sum is rot_dim / 2), e.g. frames, rows and columns of a video. */
+    int n_axes;
+    int sections[4];
+    float magnitude; /* scale of the rotated part (1: none) */
+    /* Device array of positions, element (b, s, axis) at b * pos_stride_b +
+     * s * pos_stride_s + axis * pos_stride_axis (strides of 0 broadcast; any
+     * sign of position).  NULL (one axis only): position = offset + s. */
+    const int64_t* positions;
+    int64_t pos_stride_b, pos_stride_s, pos_stride_axis;
+    int64_t offset;
+} ctx_rope_t;
+
+/* q_out, k_out = the rotated q, k. */
+int ctx_rope_fwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_rope_t* rope, ctx_dtype_t dtype,
+                 ctx_layout_t layout, const ctx_tensor_t* q_out, const ctx_tensor_t* k_out, ctx_stream_t stream);
+/* Its gradient: dq, dk from dq_out, dk_out (the transposed rotation, so the
+ * inverse one when magnitude is 1). */
+int ctx_rope_bwd(const ctx_tensor_t* dq_out, const ctx_tensor_t* dk_out, const ctx_rope_t* rope, ctx_dtype_t dtype,
+                 ctx_layout_t layout, const ctx_tensor_t* dq, const ctx_tensor_t* dk, ctx_stream_t stream);
+
+/* Every head's row is divided by its root mean square and multiplied by the
+ * weights, then rotated, in one pass:
+ *   x -> R(x / sqrt(mean(x^2) + eps) * w).
+ * wq, wk: device arrays [D] of w_dtype, or NULL (all ones); rope: NULL for
+ * the norm alone. */
+int ctx_qk_norm_rope_fwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const void* wq, const void* wk,
+                         ctx_dtype_t w_dtype, float eps, const ctx_rope_t* rope, ctx_dtype_t dtype,
+                         ctx_layout_t layout, const ctx_tensor_t* q_out, const ctx_tensor_t* k_out,
+                         ctx_stream_t stream);
+/* Its gradients from dq_out, dk_out and the forward's inputs q, k (row
+ * statistics are recomputed, nothing is saved).  dwq, dwk: fp32 [D] summed
+ * over batch, sequence and heads, written (not added to), or NULL; they need
+ * their weights.  The sums run in a fixed order: equal calls give equal bits.
+ * workspace: ctx_qk_norm_rope_workspace_size(D) bytes, 256-byte aligned, when
+ * dwq or dwk is wanted (else it may be NULL). */
+int ctx_qk_norm_rope_bwd(const ctx_tensor_t* dq_out, const ctx_tensor_t* dk_out, const ctx_tensor_t* q,
+                         const ctx_tensor_t* k, const void* wq, const void* wk, ctx_dtype_t w_dtype, float eps,
+                         const ctx_rope_t* rope, ctx_dtype_t dtype, ctx_layout_t layout, const ctx_tensor_t* dq,
+                         const ctx_tensor_t* dk, float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
+                         ctx_stream_t stream);
+size_t ctx_qk_norm_rope_workspace_size(int D);
+
 /* Synchronises the stream, then returns and clears the device status word
  * that kernels set when a bounded wait ran out (CTX_ERR_TIMEOUT) or CTX_OK;
  * CTX_ERR_CUDA if the synchronisation itself failed. */
