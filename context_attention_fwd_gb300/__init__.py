@@ -24,7 +24,7 @@ import torch
 from . import build as _build
 
 __all__ = [
-    "attn_fwd", "attn_bwd", "seq_head_exchange", "exchanged_view", "workspace_size",
+    "attn_fwd", "attn_bwd", "attn_window_fwd", "attn_window_bwd", "window_workspace_size", "seq_head_exchange", "exchanged_view", "workspace_size",
     "chunk_offsets", "device_status", "selftest_wait_timeout", "library_path", "load_library",
     "profile_enable", "profile_read", "launch_plan", "debug_set", "kernel_binary_version",
     "RopeTable", "rope_table", "rope_fwd", "rope_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
@@ -97,6 +97,10 @@ def load_library(build_if_missing: bool = True):
             lib.ctx_attn_launch_plan.argtypes = [I, I, I, I, I, I, P(I), I, P(_Plan)]
             lib.ctx_debug_set.argtypes = [ctypes.c_uint, ctypes.c_uint]
             lib.ctx_kernel_binary_version.argtypes = [P(I)]
+            lib.ctx_attn_window_fwd.argtypes = [T, T, T, I, P(I), I, I, I, I, I, F, T, V, V]
+            lib.ctx_attn_window_bwd.argtypes = [T, T, T, T, V, T, I, P(I), I, I, I, I, I, F, T, T, T, V, SZ, V]
+            lib.ctx_attn_window_workspace_size.argtypes = [I] * 10
+            lib.ctx_attn_window_workspace_size.restype = SZ
             R = P(_Rope)
             lib.ctx_rope_fwd.argtypes = [T, T, R, I, I, T, T, V]
             lib.ctx_rope_bwd.argtypes = [T, T, R, I, I, T, T, V]
@@ -110,7 +114,7 @@ def load_library(build_if_missing: bool = True):
                       "ctx_get_device_status", "ctx_selftest_wait_timeout", "ctx_profile_enable",
                       "ctx_profile_read", "ctx_selftest_exp2", "ctx_attn_launch_plan", "ctx_debug_set",
                       "ctx_kernel_binary_version", "ctx_rope_fwd", "ctx_rope_bwd", "ctx_qk_norm_rope_fwd",
-                      "ctx_qk_norm_rope_bwd"):
+                      "ctx_qk_norm_rope_bwd", "ctx_attn_window_fwd", "ctx_attn_window_bwd"):
                 getattr(lib, n).restype = I
             _lib = lib
     return _lib
@@ -265,6 +269,70 @@ def attn_bwd(q, k, v, out, lse, dout, P, chunk_offsets=None, causal=False, scale
                           ctypes.byref(_desc(dk)), ctypes.byref(_desc(dv)),
                           ctypes.c_void_p(ws.data_ptr()), wsb, _stream(q))
     _check(rc, "ctx_attn_bwd")
+    return dq, dk, dv
+
+
+def _window(window, sinks):
+    """(left, right, sinks) of a call: an int is both sides, -1 unlimited."""
+    left, right = (window, window) if isinstance(window, int) else window
+    if left < -1 or right < -1 or sinks < 0:
+        raise ValueError(f"window sides must be >= -1 and sinks >= 0, got {window}, {sinks}")
+    big = (1 << 31) - 1
+    return min(int(left), big), min(int(right), big), min(int(sinks), big)
+
+
+def window_workspace_size(B, S, Hq, Hkv, D, P, window, sinks=0, causal=False) -> int:
+    """Bytes of device workspace ``attn_window_bwd`` needs for these sizes."""
+    return int(load_library().ctx_attn_window_workspace_size(B, S, Hq, Hkv, D, P, int(causal), *_window(window, sinks)))
+
+
+def attn_window_fwd(q, k, v, P, window, sinks=0, chunk_offsets=None, causal=False, scale=None, out=None, lse=None):
+    """Attention forward under a sliding window with sink tokens -> (out, lse)
+    as ``attn_fwd`` returns them.
+
+    ``window`` (left, right), or one int for both: query i sees keys i - left
+    .. i + right (-1: unlimited; causal: nothing after i), and the first
+    ``sinks`` keys of the sequence.  A causal window of W tokens, the query's
+    own among them, is (W - 1, 0)."""
+    lib = load_library()
+    named = [("q", q), ("k", k), ("v", v)] + ([("out", out)] if out is not None else [])
+    _check_types(named)
+    B, S, Hq, D = q.shape
+    _check_inputs(named, q.device, lse, (B, Hq, S))
+    left, right, sinks = _window(window, sinks)
+    out = _like_layout(q, Hq) if out is None else out
+    lse = torch.empty(B, Hq, S, dtype=torch.float32, device=q.device) if lse is None else lse
+    with _on(q.device):
+        rc = lib.ctx_attn_window_fwd(ctypes.byref(_desc(q)), ctypes.byref(_desc(k)), ctypes.byref(_desc(v)), P,
+                                     _offsets(P, chunk_offsets), LAYOUT_BSHD, int(causal), left, right, sinks,
+                                     float(scale) if scale else 0.0, ctypes.byref(_desc(out)), _ptr(lse), _stream(q))
+    _check(rc, "ctx_attn_window_fwd")
+    return out, lse
+
+
+def attn_window_bwd(q, k, v, out, lse, dout, P, window, sinks=0, chunk_offsets=None, causal=False, scale=None,
+                    dq=None, dk=None, dv=None, workspace=None):
+    """Gradients through ``attn_window_fwd`` -> (dq, dk, dv) bf16, stored like q / k."""
+    lib = load_library()
+    named = [("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout)]
+    named += [(n, t) for n, t in (("dq", dq), ("dk", dk), ("dv", dv)) if t is not None]
+    _check_types(named)
+    B, S, Hq, D = q.shape
+    Hkv = k.shape[2]
+    _check_inputs(named, q.device, lse, (B, Hq, S))
+    left, right, sinks = _window(window, sinks)
+    dq = _like_layout(q, Hq) if dq is None else dq
+    dk = _like_layout(k, Hkv) if dk is None else dk
+    dv = _like_layout(k, Hkv) if dv is None else dv
+    nbytes = lib.ctx_attn_window_workspace_size(B, S, Hq, Hkv, D, P, int(causal), left, right, sinks)
+    ws, wsb = _workspace(nbytes, q.device, workspace)
+    with _on(q.device):
+        rc = lib.ctx_attn_window_bwd(ctypes.byref(_desc(q)), ctypes.byref(_desc(k)), ctypes.byref(_desc(v)),
+                                     ctypes.byref(_desc(out)), _ptr(lse), ctypes.byref(_desc(dout)), P,
+                                     _offsets(P, chunk_offsets), LAYOUT_BSHD, int(causal), left, right, sinks,
+                                     float(scale) if scale else 0.0, ctypes.byref(_desc(dq)), ctypes.byref(_desc(dk)),
+                                     ctypes.byref(_desc(dv)), _ptr(ws), wsb, _stream(q))
+    _check(rc, "ctx_attn_window_bwd")
     return dq, dk, dv
 
 

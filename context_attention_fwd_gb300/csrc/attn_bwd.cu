@@ -100,7 +100,16 @@ __device__ __forceinline__ void red_add_v4(float* addr, float a, float b, float 
                  : "memory");
 }
 
-template <int D, bool kHeadMajor>
+// 32 fp32 columns of a partial dK / dV row, summed by sink_reduce_kernel.
+__device__ __forceinline__ void store_part(float* dst, const uint32_t* o) {
+    float4* d4 = reinterpret_cast<float4*>(dst);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        d4[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                            __uint_as_float(o[4 * k + 3]));
+}
+
+template <int D, bool kHeadMajor, bool kWindow>
 __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_constant__ BwdParams p) {
     griddep_wait();  // the previous kernel in the stream is complete (launch_kernel)
     griddep_launch_dependents();
@@ -113,15 +122,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     const float* stat_base = reinterpret_cast<const float*>(smem + L::OFF_STAT);
     const int warp = warp_id(), lane = lane_id();
     const GridPos gp = grid_pos<kHeadMajor>();
-    const int kt = gp.tile, hk = gp.head, b = gp.z;
+    const WinWork ww = kWindow ? win_work(gp.tile, p.sink_tiles, p.sink_parts) : WinWork{gp.tile, -1};
+    const int kt = ww.kv_tile, hk = gp.head, b = gp.z;
     const ChunkTable& ct = p.ct;
     const int c = chunk_of_tile(ct, kt);
     const int kv_start = ct.off[c] + (kt - ct.tile_off[c]) * kTile;
     const int kv_len = min(kTile, ct.off[c + 1] - kv_start);
     const int G = p.group;
-    const QWalk qw{&ct, c, p.causal, kv_start, hk * G + G};
+    const auto qw = [&] {
+        if constexpr (kWindow) {
+            const WinQ q = ww.part < 0 ? win_near_q(ct, p.win, p.S, kv_start, kv_start + kv_len)
+                                       : win_part_q(ct, p.win, kt, ww.part, p.sink_per);
+            return WinQWalk{&ct, q, q.t0 < ct.ntiles ? chunk_of_tile(ct, q.t0) : 0, hk * G + G};
+        } else {
+            return QWalk{&ct, c, p.causal, kv_start, hk * G + G};
+        }
+    }();
     const int n_q = qw.count(G);  // query tiles this CTA visits (all heads of the group)
     const WaitCtx wc{&bars.abort_flag, p.status, p.timeout_ns};
+    if (kWindow && n_q == 0) return;  // a part past the last query tile
+    // windowed sink tiles: fp32 partial rows of this part, and how many it writes
+    float* part_row = nullptr;
+    int part_rows = 0;
+    if constexpr (kWindow) {
+        if (ww.part >= 0 && p.dkv_part) {
+            part_row = p.dkv_part + ((((size_t)ww.part * p.B + b) * p.Hkv + hk) * p.sink_rows + kv_start) * 2 * D;
+            part_rows = win_overlap(qw.q, win_near_q(ct, p.win, p.S, kv_start, kv_start + kv_len))
+                            ? kv_len : min(kv_len, p.win.sinks - kv_start);
+        }
+    }
 
     if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment
         if (threadIdx.x == 0) atomicExch(p.status, 2);
@@ -306,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             const int st = i & 1, ph = (i >> 1) & 1;
             // causal diagonal tile: query columns before this thread's key are masked
             const int q_start = q_first_row(q);
-            const bool diag = p.causal && q.r == c && kv_start + kv_len - 1 > q_start;
+            const bool diag = !kWindow && p.causal && q.r == c && kv_start + kv_len - 1 > q_start;
             const int lo = diag ? kv_start + row - q_start - half * 64 : 0;  // mask columns k < lo
             const float4* nlse2 = reinterpret_cast<const float4*>(stat_base + st * 256 + half * 64);
             const float4* delta = reinterpret_cast<const float4*>(stat_base + st * 256 + 128 + half * 64);
@@ -329,7 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
                 pr[4 * k4 + 2] = __float_as_uint(ex2(x1.x));
                 pr[4 * k4 + 3] = __float_as_uint(ex2(x1.y));
             }
-            if (diag || kv_len < kTile) {  // tile-uniform: only edge tiles pay for masking
+            if constexpr (kWindow) {
+                zero_window(p.win, q_start, q_start + half * 64, row, kv_start, kv_len, pr);
+            } else if (diag || kv_len < kTile) {  // tile-uniform: only edge tiles pay for masking
                 const int lo_eff = row_valid ? lo : 64;  // zero columns k < lo_eff
 #pragma unroll
                 for (int k = 0; k < 64; ++k)
@@ -393,7 +424,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             for (int cc = 0; cc < kHalfCols / 32; ++cc) {
                 uint32_t o[32];
                 tmem_ld32_sync(taddr + L::TM_DV + half * kHalfCols + cc * 32, o);
-                if (row_valid) {
+                if (kWindow && part_row) {
+                    if (row < part_rows)
+                        store_part(part_row + ((size_t)row * 2 + 1) * D + half * kHalfCols + cc * 32, o);
+                } else if (row_valid) {
                     uint4* d4 = reinterpret_cast<uint4*>(dst + cc * 32);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -444,7 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
             for (int cc = 0; cc < D / 32; ++cc) {
                 uint32_t o[32];
                 tmem_ld32_sync(taddr + L::TM_DK + cc * 32, o);
-                if (row_valid) {
+                if (kWindow && part_row) {  // unscaled
+                    if (row < part_rows) store_part(part_row + (size_t)row * 2 * D + cc * 32, o);
+                } else if (row_valid) {
                     uint4* d4 = reinterpret_cast<uint4*>(dst + cc * 32);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -464,23 +500,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     if (warp == kMmaWarp) tmem_dealloc(tmem, L::TM_COLS);
 }
 
-template <int D, bool kHeadMajor>
+template <int D, bool kHeadMajor, bool kWindow>
 int launch_bwd_do(const BwdParams& p, cudaStream_t s) {
     using L = BwdLayout<D>;
     static OncePerDevice attr;
     if (!attr.run([] {
-            return cudaFuncSetAttribute(attn_bwd_kernel<D, kHeadMajor>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(attn_bwd_kernel<D, kHeadMajor, kWindow>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         L::SMEM) == cudaSuccess;
         }))
         return 4;
-    const cudaError_t e = launch_kernel(p.pdl != 0, attn_bwd_kernel<D, kHeadMajor>,
-                                        grid_dims(kHeadMajor, p.ct.ntiles, p.Hkv, p.B), dim3(kThreads), L::SMEM, s, p);
+    const int tiles = kWindow ? win_grid(p.ct.ntiles, p.sink_tiles, p.sink_parts) : p.ct.ntiles;
+    const cudaError_t e = launch_kernel(p.pdl != 0, attn_bwd_kernel<D, kHeadMajor, kWindow>,
+                                        grid_dims(kHeadMajor, tiles, p.Hkv, p.B), dim3(kThreads), L::SMEM, s, p);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : 4;
 }
 
 template <int D>
 int launch_bwd_d(const BwdParams& p, cudaStream_t s) {
-    return p.head_major ? launch_bwd_do<D, true>(p, s) : launch_bwd_do<D, false>(p, s);
+    if (p.windowed) return launch_bwd_do<D, false, true>(p, s);
+    return p.head_major ? launch_bwd_do<D, true, false>(p, s) : launch_bwd_do<D, false, false>(p, s);
 }
 
 }  // namespace

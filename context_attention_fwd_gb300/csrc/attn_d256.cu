@@ -80,7 +80,7 @@ struct F256Bars {
 constexpr int kF256Threads = 256;
 constexpr float kRescaleThreshold = 8.0f;
 
-template <bool kPartials, bool kHeadMajor>
+template <bool kPartials, bool kHeadMajor, bool kWindow>
 __global__ void __launch_bounds__(kF256Threads, 1) attn_fwd256_kernel(const __grid_constant__ FwdParams p) {
     griddep_wait();  // the previous kernel in the stream is complete (launch_kernel)
     griddep_launch_dependents();
@@ -102,7 +102,17 @@ __global__ void __launch_bounds__(kF256Threads, 1) attn_fwd256_kernel(const __gr
     const int q_rows = min(kTile, ct.off[r + 1] - q_start);
     const int hk = h / p.group;
     const WalkCfg g{r, ct.P, p.causal, p.allgather, q_start + q_rows - 1};
-    const int n_kv = kv_count(ct, g);
+    WinKv wk;
+    if constexpr (kWindow) wk = win_kv(ct, p.win, p.S, q_start, g.q_last);
+    const int n_kv = kWindow ? wk.count() : kv_count(ct, g);
+    auto walk_first = [&](KvWalk& w) {
+        if constexpr (kWindow) win_first(ct, wk, w);
+        else kv_first(ct, g, w);
+    };
+    auto walk_next = [&](KvWalk& w) {
+        if constexpr (kWindow) win_next(ct, wk, w);
+        else kv_next(ct, g, w);
+    };
     const WaitCtx wc{&abort_flag, p.status, p.timeout_ns};
 
     if (threadIdx.x == 0) {
@@ -155,8 +165,8 @@ __global__ void __launch_bounds__(kF256Threads, 1) attn_fwd256_kernel(const __gr
             bool ok = true;
             const int skip = debug_skip_step(p.debug, n_kv);  // -1 in normal use
             KvWalk w;
-            kv_first(ct, g, w);
-            for (int j = 0; j < n_kv && ok; ++j, kv_next(ct, g, w)) {
+            walk_first(w);
+            for (int j = 0; j < n_kv && ok; ++j, walk_next(w)) {
                 if (j == skip) {  // failure injection: no K, V from step j on
                     ok = false;
                     break;
@@ -231,8 +241,8 @@ __global__ void __launch_bounds__(kF256Threads, 1) attn_fwd256_kernel(const __gr
                 drain_wait(smem_u32(&bars.drain_s), 0, p.timeout_ns);
             } else {
                 KvWalk w;
-                kv_first(ct, g, w);
-                for (int j = 0; j < n_kv && ok; ++j, kv_next(ct, g, w)) {
+                walk_first(w);
+                for (int j = 0; j < n_kv && ok; ++j, walk_next(w)) {
                     const bool first_c = w.t == w.t0, last_c = kv_chunk_last(ct, g, w);
                     const bool acc0 = kPartials ? !first_c : j > 0;
                     if (!(ok = mbar_wait(smem_u32(&bars.p_full[j & 1]), (j >> 1) & 1, wc))) break;
@@ -270,8 +280,8 @@ __global__ void __launch_bounds__(kF256Threads, 1) attn_fwd256_kernel(const __gr
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
         KvWalk w;
-        kv_first(ct, g, w);
-        for (int j = 0; j < n_kv; ++j, kv_next(ct, g, w)) {
+        walk_first(w);
+        for (int j = 0; j < n_kv; ++j, walk_next(w)) {
             const int kv_start = ct.off[w.c] + (w.t - w.t0) * kTile;
             const int kv_len = min(kTile, ct.off[w.c + 1] - kv_start);
             const bool first = kPartials ? (w.t == w.t0) : (j == 0);
@@ -282,7 +292,9 @@ __global__ void __launch_bounds__(kF256Threads, 1) attn_fwd256_kernel(const __gr
             tc_fence_after();
             uint32_t s[128];
             tmem_ld128_sync(taddr + s_cols, s);
-            if (kv_len < kTile || diag) {
+            if constexpr (kWindow) {
+                mask_window(p.win, q_start, row, kv_start, kv_len, s);
+            } else if (kv_len < kTile || diag) {
 #pragma unroll
                 for (int k = 0; k < 128; ++k)
                     if (k >= lim) s[k] = __float_as_uint(-INFINITY);
@@ -450,7 +462,7 @@ __device__ __forceinline__ void red_add_v4(float* addr, float a, float b, float 
 // Q_h is read by S part B and dK, dO_h by dP part B and dV: a slot is free
 // once each product that reads it has completed (two releases per load, one
 // per reader), whichever thread then refills it.
-template <bool kHeadMajor>
+template <bool kHeadMajor, bool kWindow>
 __global__ void __launch_bounds__(kB256Threads, 1) attn_bwd256_kernel(const __grid_constant__ BwdParams p) {
     griddep_wait();  // the previous kernel in the stream is complete (launch_kernel)
     griddep_launch_dependents();
@@ -466,7 +478,9 @@ __global__ void __launch_bounds__(kB256Threads, 1) attn_bwd256_kernel(const __gr
     // there the two column halves of a KV tile are launched side by side and
     // stream the same Q, dO and V tiles at the same time, so the second read
     // of each tile hits in L2.
-    const int kt = kHeadMajor ? (int)blockIdx.z : (int)(blockIdx.x >> 1);
+    const int tile = kHeadMajor ? (int)blockIdx.z : (int)(blockIdx.x >> 1);
+    const WinWork ww = kWindow ? win_work(tile, p.sink_tiles, p.sink_parts) : WinWork{tile, -1};
+    const int kt = ww.kv_tile;
     const int hk = kHeadMajor ? (int)blockIdx.x : (int)blockIdx.y;
     const int hh = kHeadMajor ? (int)(blockIdx.y & 1) : (int)(blockIdx.x & 1);
     const int zs = kHeadMajor ? (int)(blockIdx.y >> 1) : (int)blockIdx.z;  // b * hsplit + split
@@ -477,9 +491,18 @@ __global__ void __launch_bounds__(kB256Threads, 1) attn_bwd256_kernel(const __gr
     const int kv_len = min(kTile, ct.off[c + 1] - kv_start);
     const int Gs = p.group / p.hsplit;       // query heads of this CTA
     const int h0 = hk * p.group + split * Gs;
-    const QWalk qw{&ct, c, p.causal, kv_start, h0 + Gs};
+    const auto qw = [&] {
+        if constexpr (kWindow) {
+            const WinQ q = ww.part < 0 ? win_near_q(ct, p.win, p.S, kv_start, kv_start + kv_len)
+                                       : win_part_q(ct, p.win, kt, ww.part, p.sink_per);
+            return WinQWalk{&ct, q, q.t0 < ct.ntiles ? chunk_of_tile(ct, q.t0) : 0, h0 + Gs};
+        } else {
+            return QWalk{&ct, c, p.causal, kv_start, h0 + Gs};
+        }
+    }();
     const int n_q = qw.count(Gs);
     const WaitCtx wc{&bars.abort_flag, p.status, p.timeout_ns};
+    if (kWindow && n_q == 0) return;  // a part past the last query tile
 
     if (sbase & 1023u) {
         if (threadIdx.x == 0) atomicExch(p.status, 2);
@@ -515,9 +538,16 @@ __global__ void __launch_bounds__(kB256Threads, 1) attn_bwd256_kernel(const __gr
     const uint32_t tmem = bars.tmem_slot;
     const QTileIter q0 = qw.first(h0);
     // fp32 partial rows of this CTA's (split, b, hk) when the group is split
-    float* const part_row = p.dkv_part
-        ? p.dkv_part + ((((size_t)(split * p.B + b) * p.Hkv + hk) * p.S + kv_start) * 2) * kD + hh * 128
-        : nullptr;
+    // (or, windowed, of this part of a sink tile's walk, which may only hold sink rows)
+    float* const part_row = !p.dkv_part || (kWindow && ww.part < 0)
+        ? nullptr
+        : p.dkv_part + ((((size_t)((kWindow ? ww.part : split) * p.B + b) * p.Hkv + hk) *
+                         (kWindow ? p.sink_rows : p.S) + kv_start) * 2) * kD + hh * 128;
+    int part_rows = kv_len;
+    if constexpr (kWindow) {
+        if (part_row && !win_overlap(qw.q, win_near_q(ct, p.win, p.S, kv_start, kv_start + kv_len)))
+            part_rows = min(kv_len, p.win.sinks - kv_start);
+    }
     auto slot_of = [](int n) { return n % L::SLOTS; };
     auto phase_of = [](int n) { return (n / L::SLOTS) & 1; };
     auto full_bar = [&](int n) { return smem_u32(&bars.full[n % L::SLOTS]); };
@@ -682,7 +712,7 @@ __global__ void __launch_bounds__(kB256Threads, 1) attn_bwd256_kernel(const __gr
         for (int i = 0; i < n_q; ++i, qw.next(q)) {
             const int n3 = i * L::LOADS + 3;  // carries this tile's row statistics
             const int q_start = qw.first_row(q);
-            const bool diag = p.causal && q.r == c && kv_start + kv_len - 1 > q_start;
+            const bool diag = !kWindow && p.causal && q.r == c && kv_start + kv_len - 1 > q_start;
             const int lo = diag ? kv_start + row - q_start - half * 64 : 0;
             const float4* nlse2 = reinterpret_cast<const float4*>(stat_base + (i & 1) * 256 + half * 64);
             const float4* delta = reinterpret_cast<const float4*>(stat_base + (i & 1) * 256 + 128 + half * 64);
@@ -704,7 +734,9 @@ __global__ void __launch_bounds__(kB256Threads, 1) attn_bwd256_kernel(const __gr
                 pr[4 * k4 + 2] = __float_as_uint(ex2(x1.x));
                 pr[4 * k4 + 3] = __float_as_uint(ex2(x1.y));
             }
-            if (diag || kv_len < kTile) {
+            if constexpr (kWindow) {
+                zero_window(p.win, q_start, q_start + half * 64, row, kv_start, kv_len, pr);
+            } else if (diag || kv_len < kTile) {
                 const int lo_eff = row_valid ? lo : 64;
 #pragma unroll
                 for (int k = 0; k < 64; ++k)
@@ -763,13 +795,13 @@ __global__ void __launch_bounds__(kB256Threads, 1) attn_bwd256_kernel(const __gr
             for (int cc = 0; cc < 2; ++cc) {
                 uint32_t o[32];
                 tmem_ld32_sync(taddr + L::TM_DV + half * 64 + cc * 32, o);
-                if (row_valid && part_row) {  // fp32 partial, summed by dkv_reduce_kernel
+                if (part_row && (kWindow ? row < part_rows : row_valid)) {  // fp32 partial, summed by dkv_reduce_kernel
                     float4* d4 = reinterpret_cast<float4*>(part_row + ((size_t)row * 2 + 1) * kD + half * 64 + cc * 32);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         d4[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
                                             __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                } else if (row_valid) {
+                } else if (row_valid && !(kWindow && part_row)) {
                     uint4* d4 = reinterpret_cast<uint4*>(dst + cc * 32);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -819,13 +851,13 @@ __global__ void __launch_bounds__(kB256Threads, 1) attn_bwd256_kernel(const __gr
             for (int cc = 0; cc < 4; ++cc) {
                 uint32_t o[32];
                 tmem_ld32_sync(taddr + L::TM_DK + cc * 32, o);
-                if (row_valid && part_row) {  // unscaled fp32 partial
+                if (part_row && (kWindow ? row < part_rows : row_valid)) {  // unscaled fp32 partial
                     float4* d4 = reinterpret_cast<float4*>(part_row + (size_t)row * 2 * kD + cc * 32);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         d4[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
                                             __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                } else if (row_valid) {
+                } else if (row_valid && !(kWindow && part_row)) {
                     uint4* d4 = reinterpret_cast<uint4*>(dst + cc * 32);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -849,28 +881,32 @@ __global__ void __launch_bounds__(kB256Threads, 1) attn_bwd256_kernel(const __gr
 
 int launch_attn_fwd256(const FwdParams& p, cudaStream_t s) {
     const bool partials = p.part_o != nullptr;
-    auto kern = partials ? (p.head_major ? attn_fwd256_kernel<true, true> : attn_fwd256_kernel<true, false>)
-                         : (p.head_major ? attn_fwd256_kernel<false, true> : attn_fwd256_kernel<false, false>);
-    static OncePerDevice attr[4];
-    if (!attr[(partials ? 2 : 0) + (p.head_major ? 1 : 0)].run([&] {
+    const bool heads_first = p.head_major && !p.windowed;
+    auto kern = p.windowed ? attn_fwd256_kernel<false, false, true>
+                : partials ? (heads_first ? attn_fwd256_kernel<true, true, false> : attn_fwd256_kernel<true, false, false>)
+                           : (heads_first ? attn_fwd256_kernel<false, true, false> : attn_fwd256_kernel<false, false, false>);
+    static OncePerDevice attr[5];
+    if (!attr[p.windowed ? 4 : (partials ? 2 : 0) + (heads_first ? 1 : 0)].run([&] {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F256::SMEM) == cudaSuccess;
         }))
         return 4;
-    const cudaError_t e = launch_kernel(p.pdl != 0, kern, grid_dims(p.head_major, p.ct.ntiles, p.Hq, p.B),
+    const cudaError_t e = launch_kernel(p.pdl != 0, kern, grid_dims(heads_first, p.ct.ntiles, p.Hq, p.B),
                                         dim3(kF256Threads), F256::SMEM, s, p);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : 4;
 }
 
 int launch_attn_bwd256(const BwdParams& p, cudaStream_t s) {
-    auto kern = p.head_major ? attn_bwd256_kernel<true> : attn_bwd256_kernel<false>;
-    static OncePerDevice attr[2];
-    if (!attr[p.head_major ? 1 : 0].run([&] {
+    const bool heads_first = p.head_major && !p.windowed;
+    auto kern = p.windowed ? attn_bwd256_kernel<false, true>
+                           : heads_first ? attn_bwd256_kernel<true, false> : attn_bwd256_kernel<false, false>;
+    static OncePerDevice attr[3];
+    if (!attr[p.windowed ? 2 : heads_first ? 1 : 0].run([&] {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, B256::SMEM) == cudaSuccess;
         }))
         return 4;
     // grid decode at the top of attn_bwd256_kernel
-    const dim3 grid = p.head_major ? dim3(p.Hkv, p.B * 2 * p.hsplit, p.ct.ntiles)
-                                   : dim3(2 * p.ct.ntiles, p.Hkv, p.B * p.hsplit);
+    const int tiles = p.windowed ? win_grid(p.ct.ntiles, p.sink_tiles, p.sink_parts) : p.ct.ntiles;
+    const dim3 grid = heads_first ? dim3(p.Hkv, p.B * 2 * p.hsplit, tiles) : dim3(2 * tiles, p.Hkv, p.B * p.hsplit);
     const cudaError_t e = launch_kernel(p.pdl != 0, kern, grid, dim3(kB256Threads), B256::SMEM, s, p);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : 4;
 }

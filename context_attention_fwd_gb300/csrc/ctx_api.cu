@@ -16,6 +16,7 @@
 #include "api_util.h"
 #include "internal.h"
 #include "ptx.cuh"
+#include "walk.cuh"
 
 using namespace ctxattn;
 
@@ -294,6 +295,46 @@ __global__ void dkv_reduce_kernel(const float* __restrict__ part, int hs, int B,
     *reinterpret_cast<uint4*>(dst) = v;
 }
 
+// Sums of the partial dK / dV rows of the KV tiles that hold sinks (windowed
+// backward): part [sink_parts][B][Hkv][sink_rows][2][D] fp32 (dK unscaled) ->
+// bf16 dk = scale * sum, dv = sum.  A part beyond the window's reach wrote
+// the sink rows alone, one past the last query tile nothing.  One thread per
+// 8 columns; parts are added in order.
+__global__ void sink_reduce_kernel(const __grid_constant__ BwdParams p, int D) {
+    griddep_wait();  // the previous kernel in the stream is complete (launch_kernel)
+    griddep_launch_dependents();
+    const int g8 = D / 8;
+    const int64_t n = (int64_t)p.B * p.Hkv * p.sink_rows * 2;  // (b, hk, row, which) rows of one part
+    const int64_t gt = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (gt >= n * g8) return;
+    const int64_t r = gt / g8;
+    const int k8 = (int)(gt - r * g8);
+    const int which = (int)(r & 1);
+    const int64_t bhs = r >> 1;
+    const int s = (int)(bhs % p.sink_rows);
+    const int64_t bh = bhs / p.sink_rows;
+    const int hk = (int)(bh % p.Hkv), b = (int)(bh / p.Hkv);
+    const int kt = tile_of_row(p.ct, s);
+    const int kv_start = tile_first_row(p.ct, kt);
+    const int kv_end = min(p.ct.off[chunk_of_tile(p.ct, kt) + 1], kv_start + kTile);
+    const WinQ near = win_near_q(p.ct, p.win, p.S, kv_start, kv_end);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < p.sink_parts; ++i) {
+        const WinQ q = win_part_q(p.ct, p.win, kt, i, p.sink_per);
+        if (q.t0 >= q.t1) break;
+        if (s >= p.win.sinks && !win_overlap(q, near)) continue;
+        const float4* src = reinterpret_cast<const float4*>(p.dkv_part + ((int64_t)i * n + r) * D + k8 * 8);
+        const float4 lo = src[0], hi = src[1];
+        acc[0] += lo.x; acc[1] += lo.y; acc[2] += lo.z; acc[3] += lo.w;
+        acc[4] += hi.x; acc[5] += hi.y; acc[6] += hi.z; acc[7] += hi.w;
+    }
+    const float f = which == 0 ? p.scale : 1.f;
+    uint4 v = make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
+                         pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f));
+    __nv_bfloat16* dst = (which == 0 ? p.dk : p.dv) + b * p.k_sb + (int64_t)s * p.k_ss + hk * p.k_sh + k8 * 8;
+    *reinterpret_cast<uint4*>(dst) = v;
+}
+
 // LSE merge of materialised partials: L = log sum_i exp(LSE_i),
 // O = sum_i exp(LSE_i - L) O_i.  part_o [P][B][H][S][D], part_lse [P][B][H][S].
 // With causal masking a row of chunk r has partials for iterations 0..r only
@@ -495,6 +536,281 @@ bool sizes_ok(int B, int S, int Hq, int Hkv, int D) {
     return true;
 }
 
+struct WindowArgs {
+    int left, right, sinks;
+};
+
+// A call's window (Window in internal.h): a side below 0 is unlimited.
+int make_window(const WindowArgs& a, int S, int causal, Window* w) {
+    if (a.left < -1 || a.right < -1 || a.sinks < 0) return CTX_ERR_INVALID_ARG;
+    w->left = a.left < 0 || a.left > S ? S : a.left;
+    w->right = causal ? 0 : (a.right < 0 || a.right > S ? S : a.right);
+    w->sinks = a.sinks > S ? S : a.sinks;
+    w->causal = causal ? 1 : 0;
+    return CTX_OK;
+}
+
+// Tiles that the window of one tile's rows reaches (an upper bound up to the
+// chunks' partial tiles).
+int window_tiles(const Window& w, int ntiles) {
+    const int64_t n = ((int64_t)w.left + w.right + 2 * kTile - 2) / kTile + 1;
+    return n < ntiles ? (int)n : ntiles;
+}
+
+// How the walks of the KV tiles that hold sinks are cut: parts of about the
+// length of the other tiles' walks, eight tiles at least, so that no CTA runs
+// much longer than the rest; at most 64 CTAs over all sink tiles (one each
+// from 64 sink tiles on), which also bounds the partial rows in memory.
+int sink_parts_max(const Window& w, int ntiles) {
+    int n = window_tiles(w, ntiles);
+    if (n < 8) n = 8;
+    const int by_length = (ntiles + n - 1) / n, by_count = 64 / ((w.sinks + kTile - 1) / kTile);
+    return std::max(1, std::min(by_length, by_count));
+}
+
+void plan_window_bwd(BwdParams* p, int S) {
+    const int ntiles = p->ct.ntiles;
+    p->sink_parts = 1;
+    p->sink_per = ntiles;
+    if (p->win.sinks <= 0) return;
+    p->sink_tiles = tile_of_row(p->ct, p->win.sinks - 1) + 1;
+    const int last = p->sink_tiles - 1, c = chunk_of_tile(p->ct, last);
+    p->sink_rows = std::min(p->ct.off[c + 1], tile_first_row(p->ct, last) + kTile);
+    p->sink_parts = sink_parts_max(p->win, ntiles);
+    p->sink_per = (ntiles + p->sink_parts - 1) / p->sink_parts;
+}
+
+size_t win_bwd_ws_bytes(int B, int S, int Hq, int Hkv, int D, int P, const Window& w) {
+    const size_t slots = (size_t)B * Hq * ntiles_upper(S, P) * kTile;
+    size_t part = 0;
+    if (w.sinks > 0) {
+        // enough for any chunking: sink_parts_max grows with the number of
+        // tiles, and the sink rows end with a tile that starts before the
+        // last sink does
+        const int parts = sink_parts_max(w, (int)ntiles_upper(S, P));
+        const size_t rows = std::min((size_t)S, (size_t)w.sinks + kTile);
+        if (parts > 1) part = align256((size_t)parts * B * Hkv * rows * 2 * D * 4);
+    }
+    return align256(slots * 4) * 2 + align256(slots * D * 4) + part;
+}
+
+struct WindowText {
+    char s[64];
+};
+WindowText window_text(const WindowArgs* on, const Window& w) {
+    WindowText t;
+    t.s[0] = 0;
+    if (on) snprintf(t.s, sizeof(t.s), " window=%d+%d sinks=%d", w.left, w.right, w.sinks);
+    return t;
+}
+
+// ctx_attn_fwd, and ctx_attn_window_fwd with `win` set.
+int attn_fwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tensor_t* v, int P,
+                  const int* chunk_offsets, ctx_layout_t layout, int causal, const WindowArgs* win, float scale,
+                  const ctx_tensor_t* out, float* lse, void* workspace, size_t workspace_bytes, int flags,
+                  ctx_stream_t stream) {
+    NvtxRange range(name);
+    if (!q || !k || !v || !out || !lse) return CTX_ERR_INVALID_ARG;
+    if (layout != CTX_LAYOUT_BSHD && layout != CTX_LAYOUT_SBHD) return CTX_ERR_INVALID_ARG;
+    if (flags & ~(CTX_FLAG_MATERIALIZE_PARTIALS | CTX_FLAG_KV_ALLGATHER)) return CTX_ERR_INVALID_ARG;
+    const int64_t B = q->B, S = q->S, Hq = q->H, D = q->D, Hkv = k->H;
+    if (B > INT32_MAX || S > INT32_MAX || Hq > 65535 || Hkv > 65535 || B > 65535)
+        return CTX_ERR_INVALID_ARG;
+    if (!sizes_ok((int)B, (int)S, (int)Hq, (int)Hkv, (int)D)) return CTX_ERR_INVALID_ARG;
+    if (D != 64 && D != 128 && D != 256) return CTX_ERR_UNSUPPORTED;
+    Dense dq_, dk_, dv_, do_;
+    int rc;
+    if ((rc = resolve(q, B, S, Hq, D, layout, &dq_))) return rc;
+    if ((rc = resolve(k, B, S, Hkv, D, layout, &dk_))) return rc;
+    if ((rc = resolve(v, B, S, Hkv, D, layout, &dv_))) return rc;
+    if ((rc = resolve(out, B, S, Hq, D, layout, &do_))) return rc;
+    if (reinterpret_cast<uintptr_t>(lse) & 3) return CTX_ERR_INVALID_ARG;
+    FwdParams p;
+    memset(&p, 0, sizeof(p));
+    if (win && (rc = make_window(*win, (int)S, causal, &p.win))) return rc;
+    p.windowed = win ? 1 : 0;
+    if ((rc = build_chunks((int)S, P, chunk_offsets, &p.ct))) return rc;
+    const bool partials = flags & CTX_FLAG_MATERIALIZE_PARTIALS;
+    if (partials) {
+        const size_t need = fwd_ws_bytes((int)B, (int)S, (int)Hq, (int)D, P, flags);
+        if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))
+            return CTX_ERR_WORKSPACE;
+        const size_t rows = (size_t)P * B * Hq * S;
+        p.part_o = static_cast<float*>(workspace);
+        p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(rows * D * 4));
+    }
+    if (!make_tmap_bshd(&p.tq, dq_.data, B, S, Hq, D, dq_.sb, dq_.ss, dq_.sh, 64, kTile) ||
+        !make_tmap_bshd(&p.tk, dk_.data, B, S, Hkv, D, dk_.sb, dk_.ss, dk_.sh, 64, kTile) ||
+        // D = 256 streams V in 64-row halves (each half is one PV k-range)
+        !make_tmap_bshd(&p.tv, dv_.data, B, S, Hkv, D, dv_.sb, dv_.ss, dv_.sh, 64, D == 256 ? 64 : kTile))
+        return CTX_ERR_CUDA;
+    p.B = (int)B; p.S = (int)S; p.Hq = (int)Hq; p.Hkv = (int)Hkv;
+    p.group = (int)(Hq / Hkv);
+    p.causal = causal ? 1 : 0;
+    p.allgather = (flags & CTX_FLAG_KV_ALLGATHER) ? 1 : 0;
+    p.head_major = win ? 0 : pick_head_major(p.causal, fwd_ctas(p.ct, (int)B, (int)Hq, (int)D));
+    p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)D);
+    p.scale_log2 = p.scale * 1.4426950408889634f;
+    p.out = static_cast<__nv_bfloat16*>(do_.data);
+    p.o_sb = do_.sb; p.o_ss = do_.ss; p.o_sh = do_.sh;
+    p.lse = lse;
+    p.status = status_ptr();
+    p.timeout_ns = timeout_ns();
+    p.debug = kernel_debug_bits();
+    if (!p.status) return CTX_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    p.pdl = use_pdl(fwd_ctas(p.ct, (int)B, (int)Hq, (int)D), win ? window_tiles(p.win, p.ct.ntiles) : p.ct.ntiles, s);
+    if (log_enabled())
+        fprintf(stderr,
+                "%s: B=%d S=%d Hq=%d Hkv=%d D=%d P=%d causal=%d%s order=%s partials=%d | %d query "
+                "tiles, %lld CTAs (%s), grid order %s\n",
+                name, p.B, p.S, p.Hq, p.Hkv, (int)D, P, p.causal, window_text(win, p.win).s,
+                p.allgather ? "all-gather" : "ring", partials ? 1 : 0,
+                p.ct.ntiles, (long long)fwd_ctas(p.ct, p.B, p.Hq, (int)D),
+                D == 256 ? "attn_fwd256_kernel, one tile per CTA" : "attn_fwd_kernel, two tiles per CTA",
+                p.head_major ? "head-major" : "tile-major");
+    prof_record(0, 0, s);
+    rc = launch_attn_fwd(p, (int)D, s);
+    prof_record(0, 1, s);
+    if (rc) return rc;
+    if (partials) {
+        const int64_t threads = B * Hq * S * (D / 4);
+        const int blk = 256;
+        rc = launch_status(launch_kernel(p.pdl != 0, lse_merge_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
+                                         dim3(blk), 0, s,
+            p.part_o, p.part_lse, P, (int)B, (int)Hq, (int)S, (int)D, p.out, p.o_sb, p.o_ss, p.o_sh,
+            lse, p.ct, p.causal));
+        if (rc) return rc;
+    }
+    return CTX_OK;
+}
+
+// ctx_attn_bwd, and ctx_attn_window_bwd with `win` set.
+int attn_bwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tensor_t* v,
+                  const ctx_tensor_t* out, const float* lse, const ctx_tensor_t* dout, int P,
+                  const int* chunk_offsets, ctx_layout_t layout, int causal, const WindowArgs* win, float scale,
+                  const ctx_tensor_t* dq, const ctx_tensor_t* dk, const ctx_tensor_t* dv, void* workspace,
+                  size_t workspace_bytes, ctx_stream_t stream) {
+    NvtxRange range(name);
+    if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv) return CTX_ERR_INVALID_ARG;
+    if (layout != CTX_LAYOUT_BSHD && layout != CTX_LAYOUT_SBHD) return CTX_ERR_INVALID_ARG;
+    const int64_t B = q->B, S = q->S, Hq = q->H, D = q->D, Hkv = k->H;
+    if (B > INT32_MAX || S > INT32_MAX || Hq > 65535 || Hkv > 65535 || B > 65535)
+        return CTX_ERR_INVALID_ARG;
+    if (!sizes_ok((int)B, (int)S, (int)Hq, (int)Hkv, (int)D)) return CTX_ERR_INVALID_ARG;
+    if (D != 64 && D != 128 && D != 256) return CTX_ERR_UNSUPPORTED;
+    if (D == 256 && B > 32767) return CTX_ERR_INVALID_ARG;  // grid z = 2 B (column halves)
+    Dense tq, tk, tv, to, tdo, tdq, tdk, tdv;
+    int rc;
+    if ((rc = resolve(q, B, S, Hq, D, layout, &tq))) return rc;
+    if ((rc = resolve(k, B, S, Hkv, D, layout, &tk))) return rc;
+    if ((rc = resolve(v, B, S, Hkv, D, layout, &tv))) return rc;
+    if ((rc = resolve(out, B, S, Hq, D, layout, &to))) return rc;
+    if ((rc = resolve(dout, B, S, Hq, D, layout, &tdo))) return rc;
+    if ((rc = resolve(dq, B, S, Hq, D, layout, &tdq))) return rc;
+    if ((rc = resolve(dk, B, S, Hkv, D, layout, &tdk))) return rc;
+    if ((rc = resolve(dv, B, S, Hkv, D, layout, &tdv))) return rc;
+    if (tdk.sb != tdv.sb || tdk.ss != tdv.ss || tdk.sh != tdv.sh) return CTX_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(lse) & 3) return CTX_ERR_INVALID_ARG;
+    BwdParams p;
+    memset(&p, 0, sizeof(p));
+    if ((rc = build_chunks((int)S, P, chunk_offsets, &p.ct))) return rc;
+    if (win) {
+        if ((rc = make_window(*win, (int)S, causal, &p.win))) return rc;
+        p.windowed = 1;
+        plan_window_bwd(&p, (int)S);
+    }
+    const size_t need = win ? win_bwd_ws_bytes((int)B, (int)S, (int)Hq, (int)Hkv, (int)D, P, p.win)
+                            : bwd_ws_bytes((int)B, (int)S, (int)Hq, (int)Hkv, (int)D, P);
+    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return CTX_ERR_WORKSPACE;
+    const size_t slots = (size_t)B * Hq * p.ct.ntiles * kTile;
+    char* ws = static_cast<char*>(workspace);
+    float* nlse2_t = reinterpret_cast<float*>(ws);
+    float* delta_t = reinterpret_cast<float*>(ws + align256(slots * 4));
+    float* dq_acc = reinterpret_cast<float*>(ws + 2 * align256(slots * 4));
+    int64_t bwd_ctas = 0;
+    if (win) {
+        p.hsplit = 1;
+        bwd_ctas = (int64_t)win_grid(p.ct.ntiles, p.sink_tiles, p.sink_parts) * Hkv * B * (D == 256 ? 2 : 1);
+    } else {
+        bwd_plan(p.ct, (int)S, (int)B, (int)Hq, (int)Hkv, (int)D, causal ? 1 : 0, &p.hsplit, &p.head_major,
+                 &bwd_ctas);
+    }
+    p.dkv_part = p.hsplit > 1 || p.sink_parts > 1 ? reinterpret_cast<float*>(ws + 2 * align256(slots * 4) + align256(slots * D * 4))
+                              : nullptr;
+    if (!make_tmap_bshd(&p.tq, tq.data, B, S, Hq, D, tq.sb, tq.ss, tq.sh, 64, kTile) ||
+        !make_tmap_bshd(&p.tk, tk.data, B, S, Hkv, D, tk.sb, tk.ss, tk.sh, 64, kTile) ||
+        !make_tmap_bshd(&p.tv, tv.data, B, S, Hkv, D, tv.sb, tv.ss, tv.sh, 64, kTile) ||
+        !make_tmap_bshd(&p.tdo, tdo.data, B, S, Hq, D, tdo.sb, tdo.ss, tdo.sh, 64, kTile))
+        return CTX_ERR_CUDA;
+    p.B = (int)B; p.S = (int)S; p.Hq = (int)Hq; p.Hkv = (int)Hkv;
+    p.group = (int)(Hq / Hkv);
+    p.causal = causal ? 1 : 0;
+    p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)D);
+    p.scale_log2 = p.scale * 1.4426950408889634f;
+    p.nlse2 = nlse2_t;
+    p.delta = delta_t;
+    p.dq_acc = dq_acc;
+    p.dk = static_cast<__nv_bfloat16*>(tdk.data);
+    p.dv = static_cast<__nv_bfloat16*>(tdv.data);
+    p.k_sb = tdk.sb; p.k_ss = tdk.ss; p.k_sh = tdk.sh;
+    p.status = status_ptr();
+    p.timeout_ns = timeout_ns();
+    p.debug = kernel_debug_bits();
+    if (!p.status) return CTX_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    p.pdl = D == 256 ? 0 : use_pdl(bwd_ctas, win ? window_tiles(p.win, p.ct.ntiles) : p.ct.ntiles, s);
+    if (log_enabled())
+        fprintf(stderr,
+                "%s: B=%d S=%d Hq=%d Hkv=%d D=%d P=%d causal=%d%s | %d KV tiles, %lld CTAs (%s), "
+                "GQA group split %d, grid order %s\n",
+                name, p.B, p.S, p.Hq, p.Hkv, (int)D, P, p.causal, window_text(win, p.win).s, p.ct.ntiles,
+                (long long)bwd_ctas,
+                D == 256 ? "attn_bwd256_kernel, column halves" : "attn_bwd_kernel, one KV tile per CTA",
+                p.hsplit, p.head_major ? "head-major" : "tile-major");
+    {
+        // row statistics, and the fp32 dQ accumulator zeroed
+        const int64_t threads = (int64_t)slots * (D / 8);
+        const int blk = 256;
+        rc = launch_status(launch_kernel(p.pdl != 0, bwd_stats_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
+                                         dim3(blk), 0, s,
+            static_cast<const __nv_bfloat16*>(to.data), to.sb, to.ss, to.sh,
+            static_cast<const __nv_bfloat16*>(tdo.data), tdo.sb, tdo.ss, tdo.sh, lse, nlse2_t,
+            delta_t, dq_acc, p.ct, (int)Hq, (int)S, (int)D, (int64_t)slots));
+        if (rc) return rc;
+    }
+    prof_record(1, 0, s);
+    rc = launch_attn_bwd(p, (int)D, s);
+    prof_record(1, 1, s);
+    if (rc) return rc;
+    if (p.dkv_part && win) {
+        const int64_t threads = B * Hkv * p.sink_rows * 2 * (D / 8);
+        const int blk = 256;
+        rc = launch_status(launch_kernel(p.pdl != 0, sink_reduce_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
+                                         dim3(blk), 0, s, p, (int)D));
+        if (rc) return rc;
+    } else if (p.dkv_part) {
+        const int64_t threads = B * Hkv * S * 2 * (D / 8);
+        const int blk = 256;
+        rc = launch_status(launch_kernel(p.pdl != 0, dkv_reduce_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
+                                         dim3(blk), 0, s,
+            p.dkv_part, p.hsplit, (int)B, (int)Hkv, (int)S, (int)D, p.dk, p.dv, p.k_sb, p.k_ss, p.k_sh,
+            p.scale));
+        if (rc) return rc;
+    }
+    {
+        const int64_t threads = (int64_t)slots * (D / 8);
+        const int blk = 256;
+        rc = launch_status(launch_kernel(p.pdl != 0, dq_convert_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
+                                         dim3(blk), 0, s,
+            dq_acc, static_cast<__nv_bfloat16*>(tdq.data), tdq.sb, tdq.ss, tdq.sh, p.ct, (int)Hq,
+            (int)D, p.scale, (int64_t)slots));
+        if (rc) return rc;
+    }
+    return CTX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -551,77 +867,8 @@ int ctx_attn_fwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tensor_
                  const int* chunk_offsets, ctx_layout_t layout, int causal, float scale,
                  const ctx_tensor_t* out, float* lse, void* workspace, size_t workspace_bytes,
                  int flags, ctx_stream_t stream) {
-    NvtxRange range("ctx_attn_fwd");
-    if (!q || !k || !v || !out || !lse) return CTX_ERR_INVALID_ARG;
-    if (layout != CTX_LAYOUT_BSHD && layout != CTX_LAYOUT_SBHD) return CTX_ERR_INVALID_ARG;
-    if (flags & ~(CTX_FLAG_MATERIALIZE_PARTIALS | CTX_FLAG_KV_ALLGATHER)) return CTX_ERR_INVALID_ARG;
-    const int64_t B = q->B, S = q->S, Hq = q->H, D = q->D, Hkv = k->H;
-    if (B > INT32_MAX || S > INT32_MAX || Hq > 65535 || Hkv > 65535 || B > 65535)
-        return CTX_ERR_INVALID_ARG;
-    if (!sizes_ok((int)B, (int)S, (int)Hq, (int)Hkv, (int)D)) return CTX_ERR_INVALID_ARG;
-    if (D != 64 && D != 128 && D != 256) return CTX_ERR_UNSUPPORTED;
-    Dense dq_, dk_, dv_, do_;
-    int rc;
-    if ((rc = resolve(q, B, S, Hq, D, layout, &dq_))) return rc;
-    if ((rc = resolve(k, B, S, Hkv, D, layout, &dk_))) return rc;
-    if ((rc = resolve(v, B, S, Hkv, D, layout, &dv_))) return rc;
-    if ((rc = resolve(out, B, S, Hq, D, layout, &do_))) return rc;
-    if (reinterpret_cast<uintptr_t>(lse) & 3) return CTX_ERR_INVALID_ARG;
-    FwdParams p;
-    memset(&p, 0, sizeof(p));
-    if ((rc = build_chunks((int)S, P, chunk_offsets, &p.ct))) return rc;
-    const bool partials = flags & CTX_FLAG_MATERIALIZE_PARTIALS;
-    if (partials) {
-        const size_t need = fwd_ws_bytes((int)B, (int)S, (int)Hq, (int)D, P, flags);
-        if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))
-            return CTX_ERR_WORKSPACE;
-        const size_t rows = (size_t)P * B * Hq * S;
-        p.part_o = static_cast<float*>(workspace);
-        p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(rows * D * 4));
-    }
-    if (!make_tmap_bshd(&p.tq, dq_.data, B, S, Hq, D, dq_.sb, dq_.ss, dq_.sh, 64, kTile) ||
-        !make_tmap_bshd(&p.tk, dk_.data, B, S, Hkv, D, dk_.sb, dk_.ss, dk_.sh, 64, kTile) ||
-        // D = 256 streams V in 64-row halves (each half is one PV k-range)
-        !make_tmap_bshd(&p.tv, dv_.data, B, S, Hkv, D, dv_.sb, dv_.ss, dv_.sh, 64, D == 256 ? 64 : kTile))
-        return CTX_ERR_CUDA;
-    p.B = (int)B; p.S = (int)S; p.Hq = (int)Hq; p.Hkv = (int)Hkv;
-    p.group = (int)(Hq / Hkv);
-    p.causal = causal ? 1 : 0;
-    p.allgather = (flags & CTX_FLAG_KV_ALLGATHER) ? 1 : 0;
-    p.head_major = pick_head_major(p.causal, fwd_ctas(p.ct, (int)B, (int)Hq, (int)D));
-    p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)D);
-    p.scale_log2 = p.scale * 1.4426950408889634f;
-    p.out = static_cast<__nv_bfloat16*>(do_.data);
-    p.o_sb = do_.sb; p.o_ss = do_.ss; p.o_sh = do_.sh;
-    p.lse = lse;
-    p.status = status_ptr();
-    p.timeout_ns = timeout_ns();
-    p.debug = kernel_debug_bits();
-    if (!p.status) return CTX_ERR_CUDA;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    p.pdl = use_pdl(fwd_ctas(p.ct, (int)B, (int)Hq, (int)D), p.ct.ntiles, s);
-    if (log_enabled())
-        fprintf(stderr,
-                "ctx_attn_fwd: B=%d S=%d Hq=%d Hkv=%d D=%d P=%d causal=%d order=%s partials=%d | %d query "
-                "tiles, %lld CTAs (%s), grid order %s\n",
-                p.B, p.S, p.Hq, p.Hkv, (int)D, P, p.causal, p.allgather ? "all-gather" : "ring", partials ? 1 : 0,
-                p.ct.ntiles, (long long)fwd_ctas(p.ct, p.B, p.Hq, (int)D),
-                D == 256 ? "attn_fwd256_kernel, one tile per CTA" : "attn_fwd_kernel, two tiles per CTA",
-                p.head_major ? "head-major" : "tile-major");
-    prof_record(0, 0, s);
-    rc = launch_attn_fwd(p, (int)D, s);
-    prof_record(0, 1, s);
-    if (rc) return rc;
-    if (partials) {
-        const int64_t threads = B * Hq * S * (D / 4);
-        const int blk = 256;
-        rc = launch_status(launch_kernel(p.pdl != 0, lse_merge_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
-                                         dim3(blk), 0, s,
-            p.part_o, p.part_lse, P, (int)B, (int)Hq, (int)S, (int)D, p.out, p.o_sb, p.o_ss, p.o_sh,
-            lse, p.ct, p.causal));
-        if (rc) return rc;
-    }
-    return CTX_OK;
+    return attn_fwd_call("ctx_attn_fwd", q, k, v, P, chunk_offsets, layout, causal, nullptr, scale, out, lse,
+                         workspace, workspace_bytes, flags, stream);
 }
 
 int ctx_attn_bwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tensor_t* v,
@@ -629,106 +876,36 @@ int ctx_attn_bwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tensor_
                  const int* chunk_offsets, ctx_layout_t layout, int causal, float scale,
                  const ctx_tensor_t* dq, const ctx_tensor_t* dk, const ctx_tensor_t* dv,
                  void* workspace, size_t workspace_bytes, ctx_stream_t stream) {
-    NvtxRange range("ctx_attn_bwd");
-    if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv) return CTX_ERR_INVALID_ARG;
-    if (layout != CTX_LAYOUT_BSHD && layout != CTX_LAYOUT_SBHD) return CTX_ERR_INVALID_ARG;
-    const int64_t B = q->B, S = q->S, Hq = q->H, D = q->D, Hkv = k->H;
-    if (B > INT32_MAX || S > INT32_MAX || Hq > 65535 || Hkv > 65535 || B > 65535)
-        return CTX_ERR_INVALID_ARG;
-    if (!sizes_ok((int)B, (int)S, (int)Hq, (int)Hkv, (int)D)) return CTX_ERR_INVALID_ARG;
-    if (D != 64 && D != 128 && D != 256) return CTX_ERR_UNSUPPORTED;
-    if (D == 256 && B > 32767) return CTX_ERR_INVALID_ARG;  // grid z = 2 B (column halves)
-    Dense tq, tk, tv, to, tdo, tdq, tdk, tdv;
-    int rc;
-    if ((rc = resolve(q, B, S, Hq, D, layout, &tq))) return rc;
-    if ((rc = resolve(k, B, S, Hkv, D, layout, &tk))) return rc;
-    if ((rc = resolve(v, B, S, Hkv, D, layout, &tv))) return rc;
-    if ((rc = resolve(out, B, S, Hq, D, layout, &to))) return rc;
-    if ((rc = resolve(dout, B, S, Hq, D, layout, &tdo))) return rc;
-    if ((rc = resolve(dq, B, S, Hq, D, layout, &tdq))) return rc;
-    if ((rc = resolve(dk, B, S, Hkv, D, layout, &tdk))) return rc;
-    if ((rc = resolve(dv, B, S, Hkv, D, layout, &tdv))) return rc;
-    if (tdk.sb != tdv.sb || tdk.ss != tdv.ss || tdk.sh != tdv.sh) return CTX_ERR_UNSUPPORTED;
-    if (reinterpret_cast<uintptr_t>(lse) & 3) return CTX_ERR_INVALID_ARG;
-    BwdParams p;
-    memset(&p, 0, sizeof(p));
-    if ((rc = build_chunks((int)S, P, chunk_offsets, &p.ct))) return rc;
-    const size_t need = bwd_ws_bytes((int)B, (int)S, (int)Hq, (int)Hkv, (int)D, P);
-    if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))
-        return CTX_ERR_WORKSPACE;
-    const size_t slots = (size_t)B * Hq * p.ct.ntiles * kTile;
-    char* ws = static_cast<char*>(workspace);
-    float* nlse2_t = reinterpret_cast<float*>(ws);
-    float* delta_t = reinterpret_cast<float*>(ws + align256(slots * 4));
-    float* dq_acc = reinterpret_cast<float*>(ws + 2 * align256(slots * 4));
-    int64_t bwd_ctas = 0;
-    bwd_plan(p.ct, (int)S, (int)B, (int)Hq, (int)Hkv, (int)D, causal ? 1 : 0, &p.hsplit, &p.head_major,
-             &bwd_ctas);
-    p.dkv_part = p.hsplit > 1 ? reinterpret_cast<float*>(ws + 2 * align256(slots * 4) + align256(slots * D * 4))
-                              : nullptr;
-    if (!make_tmap_bshd(&p.tq, tq.data, B, S, Hq, D, tq.sb, tq.ss, tq.sh, 64, kTile) ||
-        !make_tmap_bshd(&p.tk, tk.data, B, S, Hkv, D, tk.sb, tk.ss, tk.sh, 64, kTile) ||
-        !make_tmap_bshd(&p.tv, tv.data, B, S, Hkv, D, tv.sb, tv.ss, tv.sh, 64, kTile) ||
-        !make_tmap_bshd(&p.tdo, tdo.data, B, S, Hq, D, tdo.sb, tdo.ss, tdo.sh, 64, kTile))
-        return CTX_ERR_CUDA;
-    p.B = (int)B; p.S = (int)S; p.Hq = (int)Hq; p.Hkv = (int)Hkv;
-    p.group = (int)(Hq / Hkv);
-    p.causal = causal ? 1 : 0;
-    p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)D);
-    p.scale_log2 = p.scale * 1.4426950408889634f;
-    p.nlse2 = nlse2_t;
-    p.delta = delta_t;
-    p.dq_acc = dq_acc;
-    p.dk = static_cast<__nv_bfloat16*>(tdk.data);
-    p.dv = static_cast<__nv_bfloat16*>(tdv.data);
-    p.k_sb = tdk.sb; p.k_ss = tdk.ss; p.k_sh = tdk.sh;
-    p.status = status_ptr();
-    p.timeout_ns = timeout_ns();
-    p.debug = kernel_debug_bits();
-    if (!p.status) return CTX_ERR_CUDA;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    p.pdl = D == 256 ? 0 : use_pdl(bwd_ctas, p.ct.ntiles, s);
-    if (log_enabled())
-        fprintf(stderr,
-                "ctx_attn_bwd: B=%d S=%d Hq=%d Hkv=%d D=%d P=%d causal=%d | %d KV tiles, %lld CTAs (%s), "
-                "GQA group split %d, grid order %s\n",
-                p.B, p.S, p.Hq, p.Hkv, (int)D, P, p.causal, p.ct.ntiles, (long long)bwd_ctas,
-                D == 256 ? "attn_bwd256_kernel, column halves" : "attn_bwd_kernel, one KV tile per CTA",
-                p.hsplit, p.head_major ? "head-major" : "tile-major");
-    {
-        // row statistics, and the fp32 dQ accumulator zeroed
-        const int64_t threads = (int64_t)slots * (D / 8);
-        const int blk = 256;
-        rc = launch_status(launch_kernel(p.pdl != 0, bwd_stats_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
-                                         dim3(blk), 0, s,
-            static_cast<const __nv_bfloat16*>(to.data), to.sb, to.ss, to.sh,
-            static_cast<const __nv_bfloat16*>(tdo.data), tdo.sb, tdo.ss, tdo.sh, lse, nlse2_t,
-            delta_t, dq_acc, p.ct, (int)Hq, (int)S, (int)D, (int64_t)slots));
-        if (rc) return rc;
-    }
-    prof_record(1, 0, s);
-    rc = launch_attn_bwd(p, (int)D, s);
-    prof_record(1, 1, s);
-    if (rc) return rc;
-    if (p.dkv_part) {
-        const int64_t threads = B * Hkv * S * 2 * (D / 8);
-        const int blk = 256;
-        rc = launch_status(launch_kernel(p.pdl != 0, dkv_reduce_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
-                                         dim3(blk), 0, s,
-            p.dkv_part, p.hsplit, (int)B, (int)Hkv, (int)S, (int)D, p.dk, p.dv, p.k_sb, p.k_ss, p.k_sh,
-            p.scale));
-        if (rc) return rc;
-    }
-    {
-        const int64_t threads = (int64_t)slots * (D / 8);
-        const int blk = 256;
-        rc = launch_status(launch_kernel(p.pdl != 0, dq_convert_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
-                                         dim3(blk), 0, s,
-            dq_acc, static_cast<__nv_bfloat16*>(tdq.data), tdq.sb, tdq.ss, tdq.sh, p.ct, (int)Hq,
-            (int)D, p.scale, (int64_t)slots));
-        if (rc) return rc;
-    }
-    return CTX_OK;
+    return attn_bwd_call("ctx_attn_bwd", q, k, v, out, lse, dout, P, chunk_offsets, layout, causal, nullptr, scale,
+                         dq, dk, dv, workspace, workspace_bytes, stream);
+}
+
+int ctx_attn_window_fwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tensor_t* v, int P,
+                        const int* chunk_offsets, ctx_layout_t layout, int causal, int window_left,
+                        int window_right, int sinks, float scale, const ctx_tensor_t* out, float* lse,
+                        ctx_stream_t stream) {
+    const WindowArgs win{window_left, window_right, sinks};
+    return attn_fwd_call("ctx_attn_window_fwd", q, k, v, P, chunk_offsets, layout, causal, &win, scale, out, lse,
+                         nullptr, 0, CTX_FLAG_NONE, stream);
+}
+
+int ctx_attn_window_bwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tensor_t* v,
+                        const ctx_tensor_t* out, const float* lse, const ctx_tensor_t* dout, int P,
+                        const int* chunk_offsets, ctx_layout_t layout, int causal, int window_left,
+                        int window_right, int sinks, float scale, const ctx_tensor_t* dq,
+                        const ctx_tensor_t* dk, const ctx_tensor_t* dv, void* workspace,
+                        size_t workspace_bytes, ctx_stream_t stream) {
+    const WindowArgs win{window_left, window_right, sinks};
+    return attn_bwd_call("ctx_attn_window_bwd", q, k, v, out, lse, dout, P, chunk_offsets, layout, causal, &win,
+                         scale, dq, dk, dv, workspace, workspace_bytes, stream);
+}
+
+size_t ctx_attn_window_workspace_size(int B, int S, int Hq, int Hkv, int D, int P, int causal, int window_left,
+                                      int window_right, int sinks) {
+    Window w;
+    if (!sizes_ok(B, S, Hq, Hkv, D) || P < 1 || P > S || P > kMaxChunks) return 0;
+    if (make_window(WindowArgs{window_left, window_right, sinks}, S, causal, &w)) return 0;
+    return win_bwd_ws_bytes(B, S, Hq, Hkv, D, P, w);
 }
 
 }  // extern "C"

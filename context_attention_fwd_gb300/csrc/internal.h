@@ -87,6 +87,14 @@ __host__ __device__ inline int chunk_of_tile(const ChunkTable& ct, int t) {
     return c;
 }
 
+// Sliding window with sink keys: key j is visible to query i iff
+//   (j < sinks and (not causal or j <= i)) or i - left <= j <= i + right.
+// The host clamps left and right to [0, S], sinks to [0, S], and right to 0
+// under causal masking.
+struct Window {
+    int left, right, sinks, causal;
+};
+
 struct FwdParams {
     TmaMap tq, tk, tv;
     ChunkTable ct;
@@ -107,6 +115,8 @@ struct FwdParams {
     int head_major;  // launch order of the attention kernel (grid_pos in walk.cuh)
     int debug;       // kDebug* bits (0 in normal use)
     int pdl;         // launch with programmatic stream serialization (launch_kernel)
+    int windowed;    // the windowed instantiations, with `win`
+    Window win;
 };
 
 struct BwdParams {
@@ -134,6 +144,13 @@ struct BwdParams {
     int head_major;  // launch order of the attention kernel (grid_pos in walk.cuh)
     int debug;       // kDebug* bits (0 in normal use)
     int pdl;         // launch with programmatic stream serialization (launch_kernel)
+    // windowed calls (WinGrid in walk.cuh): the query tiles that see one of the
+    // first sink_tiles KV tiles are split over sink_parts CTAs of sink_per
+    // tiles each, which write fp32 partial dK (unscaled) / dV to dkv_part
+    // [sink_parts][B][Hkv][sink_rows][2][D] when there is more than one
+    int windowed;
+    Window win;
+    int sink_tiles, sink_parts, sink_per, sink_rows;
 };
 
 int launch_attn_fwd(const FwdParams& p, int D, cudaStream_t s);

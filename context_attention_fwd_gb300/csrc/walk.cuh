@@ -125,4 +125,152 @@ struct QWalk {
     }
 };
 
+// ------------------------------------------------------------- window walks
+// Under a window the tiles a CTA meets are at most two runs of the tile
+// numbering: those that hold sinks, then those the window reaches.  They are
+// visited in ascending order whatever the chunking (the merge gives the same
+// result in any order), and nothing outside them is touched.
+__host__ __device__ __forceinline__ int tile_of_row(const ChunkTable& ct, int row) {
+    int c = 0;
+    while (c + 1 < ct.P && ct.off[c + 1] <= row) ++c;
+    return ct.tile_off[c] + (row - ct.off[c]) / kTile;
+}
+__host__ __device__ __forceinline__ int tile_first_row(const ChunkTable& ct, int t) {
+    const int c = chunk_of_tile(ct, t);
+    return ct.off[c] + (t - ct.tile_off[c]) * kTile;
+}
+
+// KV tiles [0, a) and [b0, b1) of query rows [q_first, q_last].
+struct WinKv {
+    int a, b0, b1;
+    __host__ __device__ __forceinline__ int count() const { return a + b1 - b0; }
+};
+__host__ __device__ __forceinline__ WinKv win_kv(const ChunkTable& ct, const Window& w, int S, int q_first, int q_last) {
+    const int lo = q_first > w.left ? q_first - w.left : 0;
+    const int hi = q_last < S - 1 - w.right ? q_last + w.right : S - 1;
+    const int sinks = w.causal && w.sinks > q_last + 1 ? q_last + 1 : w.sinks;
+    WinKv r;
+    r.b0 = tile_of_row(ct, lo);
+    r.b1 = tile_of_row(ct, hi) + 1;
+    const int full = sinks > 0 ? tile_of_row(ct, sinks - 1) + 1 : 0;
+    r.a = full < r.b0 ? full : r.b0;
+    if (full > r.b1) r.b1 = full;
+    return r;
+}
+__device__ __forceinline__ void win_first(const ChunkTable& ct, const WinKv& g, KvWalk& w) {
+    w.t = g.a > 0 ? 0 : g.b0;
+    w.it = 0;
+    w.c = chunk_of_tile(ct, w.t);
+    w.t0 = ct.tile_off[w.c];
+    w.t1 = ct.tile_off[w.c + 1];
+}
+__device__ __forceinline__ void win_next(const ChunkTable& ct, const WinKv& g, KvWalk& w) {
+    if (++w.t == g.a) w.t = g.b0;
+    if (w.t >= g.b1) return;
+    while (w.t >= w.t1) {
+        ++w.c;
+        w.t0 = w.t1;
+        w.t1 = ct.tile_off[w.c + 1];
+    }
+}
+
+// Bits [0, n) of the 32-bit word that holds bits [base, base + 32).
+__device__ __forceinline__ uint32_t bits_below(int n, int base) {
+    const int k = n - base;
+    return k >= 32 ? 0xffffffffu : (k <= 0 ? 0u : (1u << k) - 1u);
+}
+
+// Masks a forward tile's 128 scores of query row q_start + row (raw fp32
+// bits).  Tiles that every row of the query tile sees whole skip it; the
+// test is the same for all of them, so a warp never diverges on it.  The
+// visible keys of a row are two runs, as bits of four words.
+__device__ __forceinline__ void mask_window(const Window& w, int q_start, int row, int kv_start, int kv_len,
+                                            uint32_t* s) {
+    if (kv_len == kTile && kv_start >= q_start + kTile - 1 - w.left && kv_start + kTile - 1 <= q_start + w.right) return;
+    const int i = q_start + row;
+    const int lo = i - w.left - kv_start, hi = min(kv_len, i + w.right + 1 - kv_start);
+    const int sink = min(kv_len, (w.causal ? min(w.sinks, i + 1) : w.sinks) - kv_start);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t m = (bits_below(hi, 32 * e) & ~bits_below(lo, 32 * e)) | bits_below(sink, 32 * e);
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (!(m >> k & 1u)) s[32 * e + k] = 0xff800000u;  // -inf
+    }
+}
+// The same for the backward's transposed tile: the probabilities of key row
+// kv_start + row against 64 queries from q0 on, set to zero where masked.
+__device__ __forceinline__ void zero_window(const Window& w, int q_start, int q0, int row, int kv_start, int kv_len,
+                                            uint32_t* pr) {
+    if (kv_len == kTile && q_start >= kv_start + kTile - 1 - w.right && q_start + kTile - 1 <= kv_start + w.left) return;
+    const int j = kv_start + row;
+    int lo = j - w.right - q0, hi = j + w.left + 1 - q0;
+    if (j < w.sinks) {
+        lo = w.causal ? j - q0 : 0;
+        hi = 64;
+    }
+    if (row >= kv_len) hi = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t m = bits_below(hi, 32 * e) & ~bits_below(lo, 32 * e);
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (!(m >> k & 1u)) pr[32 * e + k] = 0u;
+    }
+}
+
+// Query tiles of one KV tile (rows [kv_start, kv_end)): those the window
+// reaches, or all of them (causal: from its own on) if it holds sinks.
+struct WinQ {
+    int t0, t1;
+};
+__host__ __device__ __forceinline__ WinQ win_near_q(const ChunkTable& ct, const Window& w, int S, int kv_start, int kv_end) {
+    const int lo = kv_start > w.right ? kv_start - w.right : 0;
+    const int hi = kv_end - 1 < S - 1 - w.left ? kv_end - 1 + w.left : S - 1;
+    return WinQ{tile_of_row(ct, lo), tile_of_row(ct, hi) + 1};
+}
+__host__ __device__ __forceinline__ WinQ win_sink_q(const ChunkTable& ct, const Window& w, int kv_tile) {
+    return WinQ{w.causal ? kv_tile : 0, ct.ntiles};
+}
+// A windowed backward launches sink_parts CTAs for each of the first
+// sink_tiles KV tiles (those see far more queries than the others: their
+// walks are cut into pieces of about the others' length), then one CTA for
+// each of the rest.
+struct WinWork {
+    int kv_tile, part;  // part -1: the whole walk
+};
+__host__ __device__ __forceinline__ int win_grid(int ntiles, int sink_tiles, int sink_parts) {
+    return sink_tiles * sink_parts + ntiles - sink_tiles;
+}
+__device__ __forceinline__ WinWork win_work(int i, int sink_tiles, int sink_parts) {
+    const int n = sink_tiles * sink_parts;
+    return i < n ? WinWork{i / sink_parts, i % sink_parts} : WinWork{sink_tiles + i - n, -1};
+}
+__host__ __device__ __forceinline__ WinQ win_part_q(const ChunkTable& ct, const Window& w, int kv_tile, int part, int per) {
+    const WinQ all = win_sink_q(ct, w, kv_tile);
+    const int t0 = all.t0 + part * per;
+    return WinQ{t0 < all.t1 ? t0 : all.t1, t0 + per < all.t1 ? t0 + per : all.t1};
+}
+// A part outside the window's reach only touches sink rows.
+__host__ __device__ __forceinline__ bool win_overlap(const WinQ& a, const WinQ& b) { return a.t0 < b.t1 && b.t0 < a.t1; }
+
+struct WinQWalk {
+    const ChunkTable* ct;
+    WinQ q;
+    int r0, h_end;  // r0: chunk of tile q.t0
+    __device__ __forceinline__ int first_row(const QTileIter& i) const {
+        return ct->off[i.r] + (i.t - ct->tile_off[i.r]) * kTile;
+    }
+    __device__ __forceinline__ QTileIter first(int h0) const { return QTileIter{h0, q.t0, 0, r0}; }
+    __device__ __forceinline__ void next(QTileIter& i) const {
+        if (++i.t == q.t1) {
+            i.t = q.t0;
+            i.r = r0;
+            ++i.h;
+        }
+        while (i.t >= ct->tile_off[i.r + 1]) ++i.r;
+    }
+    __device__ __forceinline__ int count(int G) const { return G * (q.t1 - q.t0); }
+};
+
 }  // namespace ctxattn

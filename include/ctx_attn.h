@@ -168,6 +168,42 @@ int ctx_attn_bwd_noalloc(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx
                          const ctx_tensor_t* dq, const ctx_tensor_t* dk, const ctx_tensor_t* dv,
                          ctx_stream_t stream);
 
+/* ---- Sliding window with sink tokens --------------------------------------
+ *
+ * Attention of which a query sees only a band of keys around itself, and the
+ * first `sinks` keys of its sequence:  key j is visible to query i iff
+ *   (j < sinks and (not causal or j <= i)) or
+ *   (i - window_left <= j <= i + window_right and (not causal or j <= i)).
+ * window_left / window_right of -1 are unlimited; under causal masking
+ * window_right has no effect.  A causal window of W tokens, the query's own
+ * among them, is window_left = W - 1.  Every query sees itself, so no row is
+ * empty.  Work, and what is read of K and V, grows with S times the window,
+ * not with S^2.
+ *
+ * Everything else is as in ctx_attn_fwd / ctx_attn_bwd (layouts, chunks, GQA,
+ * head dimensions 64, 128 and 256, scale, ownership, dk and dv with equal
+ * strides); the result does not depend on P.  Like there, a 128-row tile of
+ * keys is multiplied whole, with probability 0 where masked: a non-finite
+ * value in k or v reaches every query whose tile meets its tile, also one
+ * that does not see that key. */
+int ctx_attn_window_fwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tensor_t* v, int P,
+                        const int* chunk_offsets, ctx_layout_t layout, int causal, int window_left,
+                        int window_right, int sinks, float scale, const ctx_tensor_t* out, float* lse,
+                        ctx_stream_t stream);
+/* Its gradients; out and lse are the windowed forward's.  workspace: at least
+ * ctx_attn_window_workspace_size(...) bytes of the same sizes and window,
+ * 256-byte aligned.  dq is accumulated in fp32 by reductions whose order is
+ * not fixed: two equal calls may differ in dq's last bit (dk and dv do not). */
+int ctx_attn_window_bwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tensor_t* v,
+                        const ctx_tensor_t* out, const float* lse, const ctx_tensor_t* dout, int P,
+                        const int* chunk_offsets, ctx_layout_t layout, int causal, int window_left,
+                        int window_right, int sinks, float scale, const ctx_tensor_t* dq,
+                        const ctx_tensor_t* dk, const ctx_tensor_t* dv, void* workspace,
+                        size_t workspace_bytes, ctx_stream_t stream);
+/* 0 on invalid sizes or window. */
+size_t ctx_attn_window_workspace_size(int B, int S, int Hq, int Hkv, int D, int P, int causal, int window_left,
+                                      int window_right, int sinks);
+
 /* How the attention calls of these sizes will be launched (host only, no
  * GPU needed; on a machine without one the SM count is taken as 148).
  *  fwd_ctas, bwd_ctas: CTAs of the forward and backward attention kernels.
