@@ -24,7 +24,8 @@ import torch
 from . import build as _build
 
 __all__ = [
-    "attn_fwd", "attn_bwd", "attn_window_fwd", "attn_window_bwd", "window_workspace_size", "seq_head_exchange", "exchanged_view", "workspace_size",
+    "attn_fwd", "attn_bwd", "attn_window_fwd", "attn_window_bwd", "window_workspace_size", "attn_decode",
+    "decode_workspace_size", "seq_head_exchange", "exchanged_view", "workspace_size",
     "chunk_offsets", "device_status", "selftest_wait_timeout", "library_path", "load_library",
     "profile_enable", "profile_read", "launch_plan", "debug_set", "kernel_binary_version",
     "RopeTable", "rope_table", "rope_fwd", "rope_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
@@ -101,6 +102,9 @@ def load_library(build_if_missing: bool = True):
             lib.ctx_attn_window_bwd.argtypes = [T, T, T, T, V, T, I, P(I), I, I, I, I, I, F, T, T, T, V, SZ, V]
             lib.ctx_attn_window_workspace_size.argtypes = [I] * 10
             lib.ctx_attn_window_workspace_size.restype = SZ
+            lib.ctx_attn_decode.argtypes = [T, T, T, V, I, I, I, F, T, V, V, SZ, V]
+            lib.ctx_attn_decode_workspace_size.argtypes = [I] * 8
+            lib.ctx_attn_decode_workspace_size.restype = SZ
             R = P(_Rope)
             lib.ctx_rope_fwd.argtypes = [T, T, R, I, I, T, T, V]
             lib.ctx_rope_bwd.argtypes = [T, T, R, I, I, T, T, V]
@@ -114,7 +118,8 @@ def load_library(build_if_missing: bool = True):
                       "ctx_get_device_status", "ctx_selftest_wait_timeout", "ctx_profile_enable",
                       "ctx_profile_read", "ctx_selftest_exp2", "ctx_attn_launch_plan", "ctx_debug_set",
                       "ctx_kernel_binary_version", "ctx_rope_fwd", "ctx_rope_bwd", "ctx_qk_norm_rope_fwd",
-                      "ctx_qk_norm_rope_bwd", "ctx_attn_window_fwd", "ctx_attn_window_bwd"):
+                      "ctx_qk_norm_rope_bwd", "ctx_attn_window_fwd", "ctx_attn_window_bwd",
+                      "ctx_attn_decode"):
                 getattr(lib, n).restype = I
             _lib = lib
     return _lib
@@ -334,6 +339,43 @@ def attn_window_bwd(q, k, v, out, lse, dout, P, window, sinks=0, chunk_offsets=N
                                      ctypes.byref(_desc(dv)), _ptr(ws), wsb, _stream(q))
     _check(rc, "ctx_attn_window_bwd")
     return dq, dk, dv
+
+
+def decode_workspace_size(B, T, Hq, Hkv, D, capacity, window=-1, sinks=0) -> int:
+    """Bytes of device workspace ``attn_decode`` needs for these sizes (may be 0)."""
+    left, _, sinks = _window((window, 0), sinks)
+    return int(load_library().ctx_attn_decode_workspace_size(B, T, Hq, Hkv, D, capacity, left, sinks))
+
+
+def attn_decode(q, k, v, lengths=None, window=-1, sinks=0, scale=None, out=None, lse=None, workspace=None):
+    """Attention of the newest T tokens of each sequence over its cache ->
+    (out bf16 [B,T,Hq,D] like q, lse fp32 [B,Hq,T]).
+
+    q [B,T,Hq,D]; k, v [B,capacity,Hkv,D] views of the cache, the new tokens'
+    rows included; ``lengths`` int32 [B] on the device (None: the caches are
+    full).  Query t is at position length - T + t; it sees the keys up to
+    itself, of those the last ``window`` before it (-1: all) and the first
+    ``sinks``.  A query before its sequence's start gives 0 and -inf."""
+    lib = load_library()
+    named = [("q", q), ("k", k), ("v", v)] + ([("out", out)] if out is not None else [])
+    _check_types(named)
+    B, T, Hq, D = q.shape
+    _check_inputs(named, q.device, lse, (B, Hq, T))
+    if lengths is not None and (lengths.dtype != torch.int32 or tuple(lengths.shape) != (B,)
+                                or not lengths.is_contiguous() or lengths.device != q.device):
+        raise ValueError(f"lengths: expected a contiguous int32 tensor of shape {(B,)} on {q.device}, "
+                         f"got {lengths.dtype} {tuple(lengths.shape)} on {lengths.device}")
+    left, _, sinks = _window((window, 0), sinks)
+    out = _like_layout(q, Hq) if out is None else out
+    lse = torch.empty(B, Hq, T, dtype=torch.float32, device=q.device) if lse is None else lse
+    with _on(q.device):
+        ws, wsb = _workspace(lib.ctx_attn_decode_workspace_size(B, T, Hq, k.shape[2], D, k.shape[1], left, sinks),
+                             q.device, workspace)
+        rc = lib.ctx_attn_decode(ctypes.byref(_desc(q)), ctypes.byref(_desc(k)), ctypes.byref(_desc(v)),
+                                 _ptr(lengths), LAYOUT_BSHD, left, sinks, float(scale) if scale else 0.0,
+                                 ctypes.byref(_desc(out)), _ptr(lse), _ptr(ws), wsb, _stream(q))
+    _check(rc, "ctx_attn_decode")
+    return out, lse
 
 
 def exchanged_shape(B, S, H, D, ring, ulysses, layout):

@@ -204,6 +204,30 @@ int ctx_attn_window_bwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_
 size_t ctx_attn_window_workspace_size(int B, int S, int Hq, int Hkv, int D, int P, int causal, int window_left,
                                       int window_right, int sinks);
 
+/* ---- The newest tokens over a cache -----------------------------------------
+ *
+ * Attention of the last T tokens of every sequence (one, in plain decoding)
+ * over its key/value cache.
+ *   q, out [B,T,Hq,D]; k, v [B,capacity,Hkv,D], any strides that keep rows on
+ *   16-byte boundaries (a cache stored [B,Hkv,capacity,D] is such a view);
+ *   lse [B,Hq,T] fp32 contiguous, natural log;
+ *   lengths: device int32 [B], tokens in each sequence's cache, the T newest
+ *   among them (their keys and values are already stored); NULL: capacity.
+ *   Read on the device; values are taken as if clamped to [0, capacity].
+ * Query t stands at position length - T + t and sees key j of its sequence
+ * iff j <= that position and (j < sinks or j >= position - window_left);
+ * window_left = -1 is unlimited.  Rows of the cache that no query of a
+ * sequence sees are not read, whatever they hold.  A query before the
+ * sequence's start (length < T) sees nothing: out = 0, lse = -infinity.
+ * A non-finite value in a key or value that one query of a sequence sees may
+ * reach the sequence's other queries of the call.
+ * workspace: ctx_attn_decode_workspace_size(...) bytes, 256-byte aligned (NULL
+ * when that is 0).  Equal calls give equal bits. */
+int ctx_attn_decode(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tensor_t* v, const int* lengths,
+                    ctx_layout_t layout, int window_left, int sinks, float scale, const ctx_tensor_t* out, float* lse,
+                    void* workspace, size_t workspace_bytes, ctx_stream_t stream);
+size_t ctx_attn_decode_workspace_size(int B, int T, int Hq, int Hkv, int D, int capacity, int window_left, int sinks);
+
 /* How the attention calls of these sizes will be launched (host only, no
  * GPU needed; on a machine without one the SM count is taken as 148).
  *  fwd_ctas, bwd_ctas: CTAs of the forward and backward attention kernels.

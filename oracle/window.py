@@ -48,3 +48,25 @@ def attn_bwd(q, k, v, dout, left, right, sinks, causal, scale=None):
     dk = torch.einsum("bhij,bihd->bjhd", ds, q.double())
     group = lambda t: t.unflatten(2, (k.shape[2], G)).sum(3)
     return dq, group(dk), group(dv)
+
+
+def decode(q, k, v, lengths, left, sinks, scale=None):
+    """The newest T tokens of each sequence over its cache, one row at a time:
+    (out, lse), 0 and -infinity for a row that sees nothing."""
+    B, T, Hq, D = q.shape
+    G, scale = Hq // k.shape[2], scale or 1.0 / math.sqrt(D)
+    out = torch.zeros(B, T, Hq, D, dtype=torch.float64)
+    lse = torch.full((B, Hq, T), -math.inf, dtype=torch.float64)
+    for b in range(B):
+        for t in range(T):
+            pos = int(lengths[b]) - T + t
+            if pos < 0:
+                continue
+            first = 0 if left < 0 else max(0, pos - left)
+            keys = list(range(min(sinks, first))) + list(range(first, pos + 1))
+            kk, vv = k[b, keys].double(), v[b, keys].double()
+            for h in range(Hq):
+                s = kk[:, h // G] @ q[b, t, h].double() * scale
+                lse[b, h, t] = torch.logsumexp(s, 0)
+                out[b, t, h] = torch.softmax(s, 0) @ vv[:, h // G]
+    return out, lse
