@@ -13,17 +13,18 @@
 // (g = R^T dy, gw = g w):  dx = r (gw - x r^2 mean(gw x)),  dw = sum g x r.
 // Everything between the load and the store is fp32; values are rounded once.
 //
-// Layout of the work.  A thread holds whole pairs: kVec of them per group, so
-// no element crosses threads for the rotation and a row's sums are a shuffle
-// over the L lanes that share the head.  A warp takes one token and walks
-// passes of 32 / L heads, so the sines and cosines of a token are computed
-// once for all of its query and key heads.
-//   kVec = 8: two 16-byte accesses (for 16-bit types) per thread and tensor;
-//             needs D, R multiples of 16 and 16-byte aligned rows.
-//   kVec = 1: any even D and R, any strides.
+// Layout of the work.  A thread holds whole pairs, so no element crosses
+// threads for the rotation and a row's sums are a shuffle over the L lanes
+// that share the head.  A warp takes one token and walks passes of 32 / L
+// heads; the sines and cosines of a token are computed once, by the warp
+// together, for all of its query and key heads.
+//   16-byte groups: eight pairs per thread, two 16-byte accesses (for 16-bit
+//     types) per tensor; needs D, R multiples of 16 and 16-byte aligned rows.
+//   single pairs: any even D and R, any strides; one head per pass.
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -37,7 +38,9 @@ namespace ctxattn {
 namespace {
 
 constexpr int kMaxRopeDim = 512;
-constexpr int kWarps = 8;  // warps of a block
+constexpr int kWarps = 8;      // warps of a forward block
+constexpr int kGradWarps = 4;  // warps of a norm-gradient block
+constexpr int kGradBlocks = 3;  // of them on an SM
 constexpr int kMaxGradBlocks = 1024;  // blocks of the backward that leave partial weight gradients
 
 enum { kRotate = 0, kNorm = 1, kNormGrad = 2 };
@@ -62,7 +65,7 @@ struct RopeParams {
     int n_axes, sec_end[4];     // pairs [sec_end[a-1], sec_end[a]) use axis a
     int interleaved;
     float m, sin_sign, eps;
-    float* dw_part;             // [blocks][2][D], or null
+    float* dw_part;             // [blocks][2][D], or null (a side without a tensor is not written)
     float* dw[2];
 };
 
@@ -83,274 +86,485 @@ __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// N consecutive elements as stored (N = 8: 16-byte accesses).
-template <typename T, int N>
-struct Chunk {
-    T e[N];
-    __device__ __forceinline__ void load(const T* p) {
-        if constexpr (N == 8) {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) * N / 16; ++i)
-                reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
-        } else {
-            e[0] = *p;
-        }
-    }
-    __device__ __forceinline__ void store(T* p) const {
-        if constexpr (N == 8) {
-#pragma unroll
-            for (int i = 0; i < (int)sizeof(T) * N / 16; ++i)
-                reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(e)[i];
-        } else {
-            *p = e[0];
-        }
-    }
-};
-
-// Where group g's two chunks of kVec elements start.  Rotated pairs in the
-// half layout: g and R/2 + g; otherwise 2 kVec consecutive elements.
-template <int kVec>
-__device__ __forceinline__ int2 chunk_at(int g, int rot, int interleaved) {
-    const bool split = !interleaved && g * kVec < rot / 2;
-    return split ? make_int2(g * kVec, rot / 2 + g * kVec) : make_int2(2 * g * kVec, 2 * g * kVec + kVec);
-}
-
-// The pairs (a[j], b[j]) of a group, from its two chunks and back.  In the
-// interleaved layout (and in the part that is not rotated, where the pairing
-// is of no consequence) a pair is two neighbouring elements.
-template <typename T, int kVec>
-__device__ __forceinline__ void unpack(const Chunk<T, kVec>& c0, const Chunk<T, kVec>& c1, bool inter, float* a,
-                                       float* b) {
-    if (kVec == 1 || !inter) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            a[j] = to_f<T>(c0.e[j]);
-            b[j] = to_f<T>(c1.e[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            a[j] = to_f<T>(2 * j < kVec ? c0.e[(2 * j) % kVec] : c1.e[(2 * j) % kVec]);
-            b[j] = to_f<T>(2 * j < kVec ? c0.e[(2 * j + 1) % kVec] : c1.e[(2 * j + 1) % kVec]);
-        }
-    }
-}
-template <typename T, int kVec>
-__device__ __forceinline__ void pack(Chunk<T, kVec>& c0, Chunk<T, kVec>& c1, bool inter, const float* a,
-                                     const float* b) {
-    if (kVec == 1 || !inter) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            c0.e[j] = from_f<T>(a[j]);
-            c1.e[j] = from_f<T>(b[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            T& ea = 2 * j < kVec ? c0.e[(2 * j) % kVec] : c1.e[(2 * j) % kVec];
-            T& eb = 2 * j < kVec ? c0.e[(2 * j + 1) % kVec] : c1.e[(2 * j + 1) % kVec];
-            ea = from_f<T>(a[j]);
-            eb = from_f<T>(b[j]);
-        }
-    }
-}
-
 __device__ __forceinline__ float weight_at(const RopeParams& p, int side, int i) {
     if (!p.w[side]) return 1.f;
     return p.w_type == CTX_DTYPE_FP32 ? static_cast<const float*>(p.w[side])[i]
          : p.w_type == CTX_DTYPE_FP16 ? __half2float(static_cast<const __half*>(p.w[side])[i])
                          : __bfloat162float(static_cast<const __nv_bfloat16*>(p.w[side])[i]);
 }
+template <typename T>
+__device__ __forceinline__ T* token_row(const RopeRows& r, int b, int s) {
+    return (T*)r.p + b * r.sb + s * r.ss;
+}
 
-// kVec pairs per group, kGroups groups per thread (lane + 32 k when kVec = 1).
-template <typename T, int kVec, int kGroups, bool kInter, int kMode>
-__global__ void __launch_bounds__(32 * kWarps) rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int N = kVec * kGroups;
-    const int lane = lane_id();
-    const int L = p.L, lig = lane & (L - 1), slot = lane >> p.log2_L, heads_per_pass = 32 >> p.log2_L;
-    const int ngroups = p.D / (2 * kVec);
-    const bool inter = kVec == 1 ? p.interleaved : kInter;
-    const int64_t units = (int64_t)p.B * p.S * p.units_per_token;
-    const int64_t nwarps = (int64_t)gridDim.x * kWarps;
+// A warp's share of the work: one token (b, s) and a range of head passes.
+struct Unit {
+    int b, s, part;
+};
+__device__ __forceinline__ Unit unit_at(const RopeParams& p, int64_t u) {
+    const int64_t token = u / p.units_per_token;
+    Unit r;
+    r.part = (int)(u - token * p.units_per_token);
+    r.b = (int)(token / p.S);
+    r.s = (int)(token - (int64_t)r.b * p.S);
+    return r;
+}
 
-    int2 at[kGroups];
-    bool live[kGroups];
-#pragma unroll
-    for (int k = 0; k < kGroups; ++k) {
-        const int g = lig + k * L;
-        live[k] = g < ngroups;
-        at[k] = chunk_at<kVec>(live[k] ? g : 0, p.rot, inter);
+// Where pair i's (cosine, sine) lies in the warp's table, in float2.  With
+// 16-byte groups a thread reads two pairs per access; the threads of a row
+// then read consecutive ones, so no two of them meet in a bank.
+template <bool kVec>
+__device__ __forceinline__ int angle_slot(int i, int ngroups) {
+    return kVec ? (((i & 7) >> 1) * ngroups + (i >> 3)) * 2 + (i & 1) : i;
+}
+
+// The cosines and sines of one token, computed by the whole warp (each angle
+// once, not once per head) and shared through `cs`.
+template <bool kVec>
+__device__ __forceinline__ void token_angles(const RopeParams& p, const Unit& u, float2* cs) {
+    __syncwarp();  // the previous token's are no longer read
+    for (int i = lane_id(); i < p.rot / 2; i += 32) {
+        int axis = 0;
+        for (int a = 0; a + 1 < p.n_axes; ++a) axis += i >= p.sec_end[a];
+        const int64_t at = p.pos ? p.pos[u.b * p.pos_sb + u.s * p.pos_ss + axis * p.pos_sa] : p.offset + u.s;
+        const int32_t turn = (int32_t)(((uint64_t)at * p.turns[i]) >> 32);
+        float si, co;
+        sincospif((float)turn * 4.656612873077393e-10f, &si, &co);  // 2^-31: half turns
+        cs[angle_slot<kVec>(i, p.D / 16)] = make_float2(co * p.m, si * p.sin_sign);
     }
-    // the style of the pairs of a group: tail groups are consecutive elements
-    float dwa[kMode == kNormGrad ? 2 : 1][N], dwb[kMode == kNormGrad ? 2 : 1][N];
-    if constexpr (kMode == kNormGrad) {
+    __syncwarp();
+}
+
+// ------------------------------------------------------- 16-byte groups
+// A thread's 16 elements of a row, as stored: eight neighbouring twos.
+// Interleaved: two j is pair j.  Half: twos 0..3 are the first elements of
+// pairs 0..7, twos 4..7 their second ones.
+template <typename T>
+struct Group {
+    uint4 u[sizeof(T)];  // 16 elements
+    __device__ __forceinline__ void load(const T* row, int2 at) {
+        constexpr int n = sizeof(T) / 2;
 #pragma unroll
-        for (int j = 0; j < N; ++j) dwa[0][j] = dwa[1][j] = dwb[0][j] = dwb[1][j] = 0.f;
+        for (int i = 0; i < n; ++i) {
+            u[i] = reinterpret_cast<const uint4*>(row + at.x)[i];
+            u[n + i] = reinterpret_cast<const uint4*>(row + at.y)[i];
+        }
     }
-
-    for (int64_t u = (int64_t)blockIdx.x * kWarps + warp_id(); u < units; u += nwarps) {
-        const int64_t token = u / p.units_per_token;
-        const int part = (int)(u - token * p.units_per_token);
-        const int b = (int)(token / p.S), s = (int)(token - (int64_t)b * p.S);
-        const int first = part * p.per_unit, last = min(first + p.per_unit, p.passes[0] + p.passes[1]);
-
-        float c[N], sn[N];
+    __device__ __forceinline__ void store(T* row, int2 at) const {
+        constexpr int n = sizeof(T) / 2;
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k)
+        for (int i = 0; i < n; ++i) {
+            reinterpret_cast<uint4*>(row + at.x)[i] = u[i];
+            reinterpret_cast<uint4*>(row + at.y)[i] = u[n + i];
+        }
+    }
+    __device__ __forceinline__ uint32_t& word(int i) { return reinterpret_cast<uint32_t*>(u)[i]; }
+    __device__ __forceinline__ uint32_t word(int i) const { return reinterpret_cast<const uint32_t*>(u)[i]; }
+    __device__ __forceinline__ float2 two(int j) const {
+        if constexpr (sizeof(T) == 4) {
+            return make_float2(__uint_as_float(word(2 * j)), __uint_as_float(word(2 * j + 1)));
+        } else if constexpr (std::is_same<T, __half>::value) {
+            const uint32_t w = word(j);
+            return __half22float2(*reinterpret_cast<const __half2*>(&w));
+        } else {
+            return make_float2(__uint_as_float(word(j) << 16), __uint_as_float(word(j) & 0xffff0000u));
+        }
+    }
+    __device__ __forceinline__ float2 swapped(int j) const {
+        const float2 v = two(j);
+        return make_float2(v.y, v.x);
+    }
+    __device__ __forceinline__ void set(int j, float2 v) {
+        if constexpr (sizeof(T) == 4) {
+            word(2 * j) = __float_as_uint(v.x);
+            word(2 * j + 1) = __float_as_uint(v.y);
+        } else if constexpr (std::is_same<T, __half>::value) {
+            const __half2 h = __floats2half2_rn(v.x, v.y);
+            word(j) = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            word(j) = pack_bf16x2(v.x, v.y);
+        }
+    }
+};
+
+struct RowThread {  // which part of which head's row a thread holds
+    int group, slot;
+    bool live;
+    int2 at;  // where its two runs of eight elements start
+    __device__ __forceinline__ RowThread(const RopeParams& p, bool inter) {
+        const int lane = lane_id();
+        slot = lane >> p.log2_L;
+        group = lane & (p.L - 1);
+        live = group < p.D / 16;
+        if (!live) group = 0;  // reads the first group's elements; kept out of sums and stores
+        at = !inter && group * 8 < p.rot / 2 ? make_int2(group * 8, p.rot / 2 + group * 8)
+                                             : make_int2(group * 16, group * 16 + 8);
+    }
+    __device__ __forceinline__ float row_sum(const RopeParams& p, float v) const {
+        if (!live) v = 0.f;
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const int i = (lig + k * L) * kVec + j;
-                c[k * kVec + j] = 1.f;
-                sn[k * kVec + j] = 0.f;
-                if (i < p.rot / 2) {
-                    int axis = 0;
-                    for (int a = 0; a + 1 < p.n_axes; ++a) axis += i >= p.sec_end[a];
-                    const int64_t at_pos = p.pos ? p.pos[b * p.pos_sb + s * p.pos_ss + axis * p.pos_sa] : p.offset + s;
-                    const int32_t turn = (int32_t)(((uint64_t)at_pos * p.turns[i]) >> 32);
-                    float si, co;
-                    sincospif((float)turn * 4.656612873077393e-10f, &si, &co);  // 2^-31: half turns
-                    c[k * kVec + j] = co * p.m;
-                    sn[k * kVec + j] = si * p.sin_sign;
-                }
+        for (int o = 1; o < 32; o <<= 1)
+            if (o < p.L) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+    // (cosine, sine) of pairs 2j, 2j + 1; 1, 0 in the part that is not rotated
+    __device__ __forceinline__ float4 angles(const RopeParams& p, const float2* cs, int j) const {
+        return group * 8 < p.rot / 2
+                   ? *reinterpret_cast<const float4*>(cs + angle_slot<true>(group * 8 + 2 * j, p.D / 16))
+                   : make_float4(1.f, 0.f, 1.f, 0.f);
+    }
+    __device__ __forceinline__ void weights(const RopeParams& p, int side, float2* w) const {
+        if (!p.w[side]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = make_float2(1.f, 1.f);
+        } else if (p.w_type == CTX_DTYPE_FP32) {
+            Group<float> g;
+            g.load(static_cast<const float*>(p.w[side]), at);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = g.two(j);
+        } else if (p.w_type == CTX_DTYPE_FP16) {
+            Group<__half> g;
+            g.load(static_cast<const __half*>(p.w[side]), at);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = g.two(j);
+        } else {
+            Group<__nv_bfloat16> g;
+            g.load(static_cast<const __nv_bfloat16*>(p.w[side]), at);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = g.two(j);
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ float row_rsqrt(float v) {
+    // 2 ulp (2^-22) is far below half a step of a 16-bit type
+    if constexpr (sizeof(T) == 4) return __frsqrt_rn(v);
+    else return rsqrtf(v);
+}
+
+// Rotation (with the norm when kNormed): one unit per warp.  Everything that a
+// token's heads share is folded into sixteen coefficients per thread, so that
+// an element costs two products and the row's factor:
+//   interleaved  y = x (wa c, wb c) + swap(x) (-wb s, wa s)
+//   half         ya = a (wa c) + b (-wb s),  yb = b (wb c) + a (wa s)
+// in two-lane fp32 instructions.  kBatch passes are loaded before the first
+// is computed, so that a warp has kBatch kilobytes (16-bit types) in flight.
+template <typename T, bool kInter, bool kNormed, int kBatch, int kBlocks>
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ __align__(16) float2 cs_all[kWarps][kMaxRopeDim / 2];
+    float2* cs = cs_all[warp_id()];
+    const int64_t un = (int64_t)blockIdx.x * kWarps + warp_id();
+    if (un >= (int64_t)p.B * p.S * p.units_per_token) return;
+    const RowThread th(p, kInter);
+    const int per_pass = 32 >> p.log2_L;
+    const float inv_d = 1.f / (float)p.D;
+    const Unit u = unit_at(p, un);
+    const int first = u.part * p.per_unit, last = min(first + p.per_unit, p.passes[0] + p.passes[1]);
+    bool have_angles = false;
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        const int base = side ? p.passes[0] : 0;
+        const int p0 = max(first - base, 0), p1 = min(last - base, p.passes[side]);
+        if (p0 >= p1) continue;
+        const T* xt = token_row<T>(p.x[side], u.b, u.s);
+        T* yt = token_row<T>(p.y[side], u.b, u.s);
+        const int64_t xh = p.x[side].sh, yh = p.y[side].sh;
+        const int H = p.H[side];
+        float2 k[16];
+        bool have_k = false;
+#pragma unroll 1
+        for (int ps = p0; ps < p1; ps += kBatch) {
+            Group<T> raw[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (ps + i < p1) raw[i].load(xt + min((ps + i) * per_pass + th.slot, H - 1) * xh, th.at);
+            if (!have_angles) {
+                token_angles<true>(p, u, cs);
+                have_angles = true;
             }
-
-        auto side_passes = [&](auto side_c) {
-            constexpr int side = decltype(side_c)::value;
-            const int p0 = max(first - (side ? p.passes[0] : 0), 0);
-            const int p1 = min(last - (side ? p.passes[0] : 0), p.passes[side]);
-            float wa[N], wb[N];
-            if (kMode != kRotate && p0 < p1) {
+            if (!have_k) {
+                float2 w[8];
+                if constexpr (kNormed) th.weights(p, side, w);
 #pragma unroll
-                for (int k = 0; k < kGroups; ++k)
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        int ia = at[k].x + j, ib = at[k].y + j;
-                        if (kVec > 1 && inter) ia = at[k].x + 2 * j, ib = ia + 1;
-                        wa[k * kVec + j] = live[k] ? weight_at(p, side, ia) : 0.f;
-                        wb[k * kVec + j] = live[k] ? weight_at(p, side, ib) : 0.f;
+                for (int j = 0; j < 4; ++j) {
+                    const float4 a = th.angles(p, cs, j);  // pairs 2j, 2j + 1
+                    if constexpr (kInter) {
+                        const float2 w0 = kNormed ? w[2 * j] : make_float2(1.f, 1.f);
+                        const float2 w1 = kNormed ? w[2 * j + 1] : make_float2(1.f, 1.f);
+                        k[2 * j] = make_float2(w0.x * a.x, w0.y * a.x);
+                        k[2 * j + 1] = make_float2(w1.x * a.z, w1.y * a.z);
+                        k[8 + 2 * j] = make_float2(-w0.y * a.y, w0.x * a.y);
+                        k[8 + 2 * j + 1] = make_float2(-w1.y * a.w, w1.x * a.w);
+                    } else {
+                        const float2 wa = kNormed ? w[j] : make_float2(1.f, 1.f);
+                        const float2 wb = kNormed ? w[4 + j] : make_float2(1.f, 1.f);
+                        k[j] = make_float2(wa.x * a.x, wa.y * a.z);
+                        k[4 + j] = make_float2(wb.x * a.x, wb.y * a.z);
+                        k[8 + j] = make_float2(-wb.x * a.y, -wb.y * a.w);
+                        k[12 + j] = make_float2(wa.x * a.y, wa.y * a.w);
                     }
+                }
+                have_k = true;
             }
-            for (int ps = p0; ps < p1; ++ps) {
-                const int h = ps * heads_per_pass + slot;
-                const bool on = h < p.H[side];
-                auto row = [&](const RopeRows& r) { return (T*)r.p + b * r.sb + s * r.ss + (int64_t)(on ? h : 0) * r.sh; };
-                Chunk<T, kVec> x0[kGroups], x1[kGroups], g0[kGroups], g1[kGroups];
-                float a[N], bb[N];
-                const T* xr = row(p.x[side]);
 #pragma unroll
-                for (int k = 0; k < kGroups; ++k) {
+            for (int i = 0; i < kBatch; ++i) {
+                if (ps + i >= p1) continue;
+                const int h = (ps + i) * per_pass + th.slot;
+                float2 r2 = make_float2(1.f, 1.f);
+                if constexpr (kNormed) {
+                    float2 q = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) a[k * kVec + j] = bb[k * kVec + j] = 0.f;
-                    if (on && live[k]) {
-                        x0[k].load(xr + at[k].x);
-                        x1[k].load(xr + at[k].y);
-                    }
+                    for (int j = 0; j < 8; ++j) q = ffma2(raw[i].two(j), raw[i].two(j), q);
+                    const float r = row_rsqrt<T>(fmaf(th.row_sum(p, q.x + q.y), inv_d, p.eps));
+                    r2 = make_float2(r, r);
                 }
-                if constexpr (kMode == kNormGrad) {
-                    const T* gr = row(p.g[side]);
+                Group<T> y;
+                if constexpr (kInter) {
 #pragma unroll
-                    for (int k = 0; k < kGroups; ++k)
-                        if (on && live[k]) {
-                            g0[k].load(gr + at[k].x);
-                            g1[k].load(gr + at[k].y);
-                        }
-                }
-#pragma unroll
-                for (int k = 0; k < kGroups; ++k)
-                    if (on && live[k]) unpack<T, kVec>(x0[k], x1[k], inter, a + k * kVec, bb + k * kVec);
-                float ya[N], yb[N];
-                if constexpr (kMode == kNormGrad) {
-                    float ga[N], gb[N], sx = 0.f, sgx = 0.f;
-#pragma unroll
-                    for (int k = 0; k < kGroups; ++k) {
-#pragma unroll
-                        for (int j = 0; j < kVec; ++j) ga[k * kVec + j] = gb[k * kVec + j] = 0.f;
-                        if (on && live[k]) unpack<T, kVec>(g0[k], g1[k], inter, ga + k * kVec, gb + k * kVec);
-                    }
-#pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        const float t = ga[j];
-                        ga[j] = t * c[j] + gb[j] * sn[j];
-                        gb[j] = gb[j] * c[j] - t * sn[j];
-                        sx = fmaf(a[j], a[j], fmaf(bb[j], bb[j], sx));
-                        sgx = fmaf(ga[j] * wa[j], a[j], fmaf(gb[j] * wb[j], bb[j], sgx));
-                    }
-                    for (int o = L >> 1; o > 0; o >>= 1) {
-                        sx += __shfl_xor_sync(0xffffffffu, sx, o);
-                        sgx += __shfl_xor_sync(0xffffffffu, sgx, o);
-                    }
-                    const float r = on ? __frsqrt_rn(sx / (float)p.D + p.eps) : 0.f;
-                    const float mean = r * r * (sgx / (float)p.D);
-#pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        dwa[side][j] = fmaf(ga[j], a[j] * r, dwa[side][j]);
-                        dwb[side][j] = fmaf(gb[j], bb[j] * r, dwb[side][j]);
-                        ya[j] = r * (ga[j] * wa[j] - a[j] * mean);
-                        yb[j] = r * (gb[j] * wb[j] - bb[j] * mean);
+                    for (int j = 0; j < 8; ++j) {
+                        float2 v = ffma2(raw[i].two(j), k[j], fmul2(raw[i].swapped(j), k[8 + j]));
+                        if constexpr (kNormed) v = fmul2(v, r2);
+                        y.set(j, v);
                     }
                 } else {
-                    if constexpr (kMode == kNorm) {
-                        float sx = 0.f;
 #pragma unroll
-                        for (int j = 0; j < N; ++j) sx = fmaf(a[j], a[j], fmaf(bb[j], bb[j], sx));
-                        for (int o = L >> 1; o > 0; o >>= 1) sx += __shfl_xor_sync(0xffffffffu, sx, o);
-                        const float r = __frsqrt_rn(sx / (float)p.D + p.eps);
-#pragma unroll
-                        for (int j = 0; j < N; ++j) {
-                            a[j] *= r * wa[j];
-                            bb[j] *= r * wb[j];
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        ya[j] = a[j] * c[j] - bb[j] * sn[j];
-                        yb[j] = bb[j] * c[j] + a[j] * sn[j];
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 a = raw[i].two(j), b = raw[i].two(4 + j);
+                        float2 va = ffma2(a, k[j], fmul2(b, k[8 + j])), vb = ffma2(b, k[4 + j], fmul2(a, k[12 + j]));
+                        if constexpr (kNormed) va = fmul2(va, r2), vb = fmul2(vb, r2);
+                        y.set(j, va);
+                        y.set(4 + j, vb);
                     }
                 }
-                T* yr = row(p.y[side]);
-#pragma unroll
-                for (int k = 0; k < kGroups; ++k)
-                    if (on && live[k]) {
-                        Chunk<T, kVec> o0, o1;
-                        pack<T, kVec>(o0, o1, inter, ya + k * kVec, yb + k * kVec);
-                        o0.store(yr + at[k].x);
-                        o1.store(yr + at[k].y);
-                    }
+                if (h < H && th.live) y.store(yt + h * yh, th.at);
             }
-        };
-        side_passes(std::integral_constant<int, 0>{});
-        side_passes(std::integral_constant<int, 1>{});
+        }
     }
+}
 
-    if constexpr (kMode == kNormGrad) {
-        if (p.dw_part) {
-            // sums over the warp's heads, then over the block's warps, in a fixed order
-            __shared__ float sm[kWarps][2 * kMaxRopeDim];
-            const int w = warp_id();
+// Gradient of the norm and the rotation.  The grid is what fits on the SMs and
+// every warp walks many tokens, all of the queries' first and then all of the
+// keys', so that the weight gradients of one side stay in its registers; each
+// block leaves its sums (over its warps, in a fixed order) for
+// weight_grad_kernel.
+template <typename T, bool kInter, int kBatch, int kBlocks>
+__global__ void __launch_bounds__(32 * kGradWarps, kBlocks) norm_grad_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ __align__(16) float2 cs_all[kGradWarps][kMaxRopeDim / 2];
+    __shared__ float sums[kGradWarps][kMaxRopeDim];
+    float2* cs = cs_all[warp_id()];
+    const RowThread th(p, kInter);
+    const int per_pass = 32 >> p.log2_L;
+    const int64_t units = (int64_t)p.B * p.S * p.units_per_token;
+    const float inv_d = 1.f / (float)p.D;
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        if (p.passes[side] == 0) continue;
+        const int H = p.H[side];
+        float2 w[8], dw[8];
+        th.weights(p, side, w);
 #pragma unroll
-            for (int side = 0; side < 2; ++side)
+        for (int j = 0; j < 8; ++j) dw[j] = make_float2(0.f, 0.f);
+        for (int64_t un = (int64_t)blockIdx.x * kGradWarps + warp_id(); un < units; un += (int64_t)gridDim.x * kGradWarps) {
+            const Unit u = unit_at(p, un);
+            // this unit's share of the side's passes
+            const int p0 = (int)((int64_t)p.passes[side] * u.part / p.units_per_token);
+            const int p1 = (int)((int64_t)p.passes[side] * (u.part + 1) / p.units_per_token);
+            if (p0 >= p1) continue;
+            const T* xt = token_row<T>(p.x[side], u.b, u.s);
+            const T* gt = token_row<T>(p.g[side], u.b, u.s);
+            T* yt = token_row<T>(p.y[side], u.b, u.s);
+            float2 c[8];  // interleaved: cos, sin of pair j; half: cos of pairs 2j, 2j + 1, then their sines
+            bool have_angles = false;
+#pragma unroll 1
+            for (int ps = p0; ps < p1; ps += kBatch) {
+                Group<T> raw[kBatch], grad[kBatch];
 #pragma unroll
-                for (int k = 0; k < kGroups; ++k)
+                for (int i = 0; i < kBatch; ++i)
+                    if (ps + i < p1) {
+                        const int h = min((ps + i) * per_pass + th.slot, H - 1);
+                        raw[i].load(xt + h * p.x[side].sh, th.at);
+                        grad[i].load(gt + h * p.g[side].sh, th.at);
+                    }
+                if (!have_angles) {
+                    token_angles<true>(p, u, cs);
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        float va = dwa[side][k * kVec + j], vb = dwb[side][k * kVec + j];
-                        for (int o = L; o < 32; o <<= 1) {
-                            va += __shfl_xor_sync(0xffffffffu, va, o);
-                            vb += __shfl_xor_sync(0xffffffffu, vb, o);
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 a = th.angles(p, cs, j);
+                        c[kInter ? 2 * j : j] = kInter ? make_float2(a.x, a.y) : make_float2(a.x, a.z);
+                        c[kInter ? 2 * j + 1 : 4 + j] = kInter ? make_float2(a.z, a.w) : make_float2(a.y, a.w);
+                    }
+                    have_angles = true;
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    if (ps + i >= p1) continue;
+                    const int h = (ps + i) * per_pass + th.slot;
+                    const bool on = h < H;
+                    float2 g[8], q = make_float2(0.f, 0.f), gq = q;
+                    if constexpr (kInter) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 v = grad[i].two(j);
+                            g[j] = make_float2(fmaf(v.x, c[j].x, v.y * c[j].y), fmaf(v.y, c[j].x, -(v.x * c[j].y)));
                         }
-                        int ia = at[k].x + j, ib = at[k].y + j;
-                        if (kVec > 1 && inter) ia = at[k].x + 2 * j, ib = ia + 1;
-                        if (live[k] && slot == 0) {
-                            sm[w][side * p.D + ia] = va;
-                            sm[w][side * p.D + ib] = vb;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 g1 = grad[i].two(j), g2 = grad[i].two(4 + j);
+                            g[j] = ffma2(g1, c[j], fmul2(g2, c[4 + j]));
+                            g[4 + j] = fsub2(fmul2(g2, c[j]), fmul2(g1, c[4 + j]));
                         }
                     }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 x = raw[i].two(j);
+                        q = ffma2(x, x, q);
+                        gq = ffma2(fmul2(g[j], x), w[j], gq);
+                    }
+                    const float sx = th.row_sum(p, q.x + q.y), sgx = th.row_sum(p, gq.x + gq.y);
+                    const float r = on ? row_rsqrt<T>(fmaf(sx, inv_d, p.eps)) : 0.f;
+                    const float kx = -r * r * r * (sgx * inv_d);
+                    const float2 r2 = make_float2(r, r), k2 = make_float2(kx, kx);
+                    Group<T> y;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 x = raw[i].two(j), gj = fmul2(g[j], r2);
+                        dw[j] = ffma2(gj, x, dw[j]);
+                        y.set(j, ffma2(gj, w[j], fmul2(x, k2)));
+                    }
+                    if (on && th.live) y.store(yt + h * p.y[side].sh, th.at);
+                }
+            }
+        }
+        if (p.dw_part) {
+            // over the warp's heads, then over the block's warps, in a fixed order
+            __syncthreads();  // the other side's sums have been read
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float va = dw[j].x, vb = dw[j].y;
+                for (int o = p.L; o < 32; o <<= 1) {
+                    va += __shfl_xor_sync(0xffffffffu, va, o);
+                    vb += __shfl_xor_sync(0xffffffffu, vb, o);
+                }
+                const int e = j < 4 ? th.at.x + 2 * j : th.at.y + 2 * (j - 4);
+                if (th.live && th.slot == 0) {
+                    sums[warp_id()][e] = va;
+                    sums[warp_id()][e + 1] = vb;
+                }
+            }
             __syncthreads();
-            for (int i = threadIdx.x; i < 2 * p.D; i += blockDim.x) {
+            for (int i = threadIdx.x; i < p.D; i += blockDim.x) {
                 float v = 0.f;
 #pragma unroll
-                for (int ww = 0; ww < kWarps; ++ww) v += sm[ww][i];
-                p.dw_part[(int64_t)blockIdx.x * 2 * p.D + i] = v;
+                for (int wi = 0; wi < kGradWarps; ++wi) v += sums[wi][i];
+                p.dw_part[((int64_t)blockIdx.x * 2 + side) * p.D + i] = v;
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------- single pairs
+// Any even D and rot_dim, any alignment: lane holds pairs lane, lane + 32, ..
+// of one head at a time; two-byte (four-byte) accesses.
+constexpr int kPairs = kMaxRopeDim / 64;
+
+template <typename T, int kMode>
+__global__ void __launch_bounds__(32 * kGradWarps) rope_pairs_kernel(const __grid_constant__ RopeParams p) {
+    __shared__ float2 cs_all[kGradWarps][kMaxRopeDim / 2];
+    __shared__ float sums[kMode == kNormGrad ? kGradWarps : 1][kMode == kNormGrad ? kMaxRopeDim : 1];
+    float2* cs = cs_all[warp_id()];
+    const int lane = lane_id(), np = p.D / 2;
+    const int64_t units = (int64_t)p.B * p.S * p.units_per_token;
+    const float inv_d = 1.f / (float)p.D;
+    int2 e[kPairs];  // elements of pair lane + 32 k
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+        const int i = min(lane + 32 * k, np - 1);
+        e[k] = !p.interleaved && i < p.rot / 2 ? make_int2(i, p.rot / 2 + i) : make_int2(2 * i, 2 * i + 1);
+    }
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+        if (p.passes[side] == 0) continue;
+        float wa[kPairs], wb[kPairs], dwa[kPairs], dwb[kPairs];
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+            dwa[k] = dwb[k] = 0.f;
+            wa[k] = kMode == kRotate ? 1.f : weight_at(p, side, e[k].x);
+            wb[k] = kMode == kRotate ? 1.f : weight_at(p, side, e[k].y);
+        }
+        for (int64_t un = (int64_t)blockIdx.x * kGradWarps + warp_id(); un < units; un += (int64_t)gridDim.x * kGradWarps) {
+            const Unit u = unit_at(p, un);
+            const int h0 = (int)((int64_t)p.H[side] * u.part / p.units_per_token);
+            const int h1 = (int)((int64_t)p.H[side] * (u.part + 1) / p.units_per_token);
+            if (h0 >= h1) continue;
+            token_angles<false>(p, u, cs);
+            for (int h = h0; h < h1; ++h) {
+                const T* x = token_row<T>(p.x[side], u.b, u.s) + h * p.x[side].sh;
+                const T* g = kMode == kNormGrad ? token_row<T>(p.g[side], u.b, u.s) + h * p.g[side].sh : x;
+                T* y = token_row<T>(p.y[side], u.b, u.s) + h * p.y[side].sh;
+                float a[kPairs], b[kPairs], ga[kPairs], gb[kPairs], sx = 0.f, sgx = 0.f;
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) {
+                    const int i = lane + 32 * k;
+                    const bool on = i < np;
+                    a[k] = on ? to_f<T>(x[e[k].x]) : 0.f;
+                    b[k] = on ? to_f<T>(x[e[k].y]) : 0.f;
+                    sx = fmaf(a[k], a[k], fmaf(b[k], b[k], sx));
+                    if constexpr (kMode == kNormGrad) {
+                        const float2 v = on && i < p.rot / 2 ? cs[i] : make_float2(1.f, 0.f);
+                        const float g1 = on ? to_f<T>(g[e[k].x]) : 0.f, g2 = on ? to_f<T>(g[e[k].y]) : 0.f;
+                        ga[k] = g1 * v.x + g2 * v.y;
+                        gb[k] = g2 * v.x - g1 * v.y;
+                        sgx = fmaf(ga[k] * wa[k], a[k], fmaf(gb[k] * wb[k], b[k], sgx));
+                    }
+                }
+                float r = 1.f;
+                if constexpr (kMode != kRotate) {
+                    for (int o = 16; o > 0; o >>= 1) {
+                        sx += __shfl_xor_sync(0xffffffffu, sx, o);
+                        if (kMode == kNormGrad) sgx += __shfl_xor_sync(0xffffffffu, sgx, o);
+                    }
+                    r = row_rsqrt<T>(fmaf(sx, inv_d, p.eps));
+                }
+                const float kx = -r * r * r * (sgx * inv_d);
+                // every element has been read: y may be x or g
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) {
+                    const int i = lane + 32 * k;
+                    if (i >= np) continue;
+                    float ya, yb;
+                    if constexpr (kMode == kNormGrad) {
+                        dwa[k] = fmaf(ga[k] * a[k], r, dwa[k]);
+                        dwb[k] = fmaf(gb[k] * b[k], r, dwb[k]);
+                        ya = fmaf(ga[k] * wa[k], r, a[k] * kx);
+                        yb = fmaf(gb[k] * wb[k], r, b[k] * kx);
+                    } else {
+                        const float2 v = i < p.rot / 2 ? cs[i] : make_float2(1.f, 0.f);
+                        const float xa = a[k] * r * wa[k], xb = b[k] * r * wb[k];
+                        ya = xa * v.x - xb * v.y;
+                        yb = xb * v.x + xa * v.y;
+                    }
+                    y[e[k].x] = from_f<T>(ya);
+                    y[e[k].y] = from_f<T>(yb);
+                }
+            }
+        }
+        if (kMode == kNormGrad && p.dw_part) {
+            __syncthreads();  // the other side's sums have been read
+#pragma unroll
+            for (int k = 0; k < kPairs; ++k)
+                if (lane + 32 * k < np) {
+                    sums[warp_id()][e[k].x] = dwa[k];
+                    sums[warp_id()][e[k].y] = dwb[k];
+                }
+            __syncthreads();
+            for (int i = threadIdx.x; i < p.D; i += blockDim.x) {
+                float v = 0.f;
+#pragma unroll
+                for (int wi = 0; wi < kGradWarps; ++wi) v += sums[kMode == kNormGrad ? wi : 0][i];
+                p.dw_part[((int64_t)blockIdx.x * 2 + side) * p.D + i] = v;
             }
         }
     }
@@ -377,11 +591,17 @@ __global__ void weight_grad_kernel(const float* __restrict__ part, int blocks, i
 
 template <typename T, int kMode>
 cudaError_t launch_rope_mode(const RopeParams& p, bool vec, unsigned grid, cudaStream_t s) {
-    const dim3 blk(32 * kWarps);
-    if (vec)
-        return p.interleaved ? launch_kernel(false, rope_kernel<T, 8, 1, true, kMode>, dim3(grid), blk, 0, s, p)
-                             : launch_kernel(false, rope_kernel<T, 8, 1, false, kMode>, dim3(grid), blk, 0, s, p);
-    return launch_kernel(false, rope_kernel<T, 1, kMaxRopeDim / 64, false, kMode>, dim3(grid), blk, 0, s, p);
+    const dim3 blk(32 * kWarps), gblk(32 * kGradWarps);
+    if (!vec) return launch_kernel(false, rope_pairs_kernel<T, kMode>, dim3(grid), gblk, 0, s, p);
+    if constexpr (kMode == kNormGrad) {
+        constexpr int kBatch = sizeof(T) == 4 ? 1 : 2;
+        return p.interleaved ? launch_kernel(false, norm_grad_kernel<T, true, kBatch, kGradBlocks>, dim3(grid), gblk, 0, s, p)
+                             : launch_kernel(false, norm_grad_kernel<T, false, kBatch, kGradBlocks>, dim3(grid), gblk, 0, s, p);
+    } else {
+        constexpr int kBatch = sizeof(T) == 4 ? 2 : kMode == kNorm ? 6 : 3, kBlocks = kMode == kNorm ? 2 : 3;
+        return p.interleaved ? launch_kernel(false, rope_kernel<T, true, kMode == kNorm, kBatch, kBlocks>, dim3(grid), blk, 0, s, p)
+                             : launch_kernel(false, rope_kernel<T, false, kMode == kNorm, kBatch, kBlocks>, dim3(grid), blk, 0, s, p);
+    }
 }
 
 template <int kMode>
@@ -438,6 +658,7 @@ int rope_call(const char* name, int mode, const ctx_tensor_t* const x[2], const 
         p.H[i] = (int)H;
         p.w[i] = w[i];
         if (w[i] && reinterpret_cast<uintptr_t>(w[i]) % (w_dtype == CTX_DTYPE_FP32 ? 4 : 2)) return CTX_ERR_UNSUPPORTED;
+        aligned = aligned && !(reinterpret_cast<uintptr_t>(w[i]) & 15);
         p.dw[i] = dw[i];
         if (dw[i] && (!w[i] || reinterpret_cast<uintptr_t>(dw[i]) % 4)) return CTX_ERR_INVALID_ARG;
     }
@@ -489,14 +710,11 @@ int rope_call(const char* name, int mode, const ctx_tensor_t* const x[2], const 
     p.per_unit = (int)((total + parts - 1) / parts);
     p.units_per_token = (total + p.per_unit - 1) / p.per_unit;
     const int64_t units = tokens * p.units_per_token;
-    int64_t grid = (units + kWarps - 1) / kWarps;
-    if (mode == kNormGrad) {
-        int64_t cap = 2LL * sms;
-        if (cap > kMaxGradBlocks) cap = kMaxGradBlocks;
-        if (grid > cap) grid = cap;
-    } else if (grid > (1LL << 30)) {
-        grid = 1LL << 30;
-    }
+    const bool walk = mode == kNormGrad || !vec;  // kernels whose warps walk many units
+    const int warps = walk ? kGradWarps : kWarps;
+    int64_t grid = (units + warps - 1) / warps;
+    if (walk) grid = std::min<int64_t>(grid, std::min<int64_t>((mode == kNormGrad ? kGradBlocks : 16LL) * sms, kMaxGradBlocks));
+    if (grid > INT32_MAX) return CTX_ERR_INVALID_ARG;
     const bool want_dw = mode == kNormGrad && (p.dw[0] || p.dw[1]);
     if (want_dw) {
         if (!workspace || workspace_bytes < ctx_qk_norm_rope_workspace_size((int)D) ||
