@@ -14,8 +14,10 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
+import struct
 import threading
 from dataclasses import dataclass
 
@@ -72,6 +74,8 @@ def library_path() -> str:
 def load_library(build_if_missing: bool = True):
     """Load libctxattn.so (building it first if asked and it is missing/stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -98,18 +102,18 @@ def load_library(build_if_missing: bool = True):
             lib.ctx_attn_launch_plan.argtypes = [I, I, I, I, I, I, P(I), I, P(_Plan)]
             lib.ctx_debug_set.argtypes = [ctypes.c_uint, ctypes.c_uint]
             lib.ctx_kernel_binary_version.argtypes = [P(I)]
-            lib.ctx_attn_window_fwd.argtypes = [T, T, T, I, P(I), I, I, I, I, I, F, T, V, V]
-            lib.ctx_attn_window_bwd.argtypes = [T, T, T, T, V, T, I, P(I), I, I, I, I, I, F, T, T, T, V, SZ, V]
+            # descriptors of the calls below are passed packed (bytes), see _PACK
+            lib.ctx_attn_window_fwd.argtypes = [V, V, V, I, P(I), I, I, I, I, I, F, V, V, V]
+            lib.ctx_attn_window_bwd.argtypes = [V, V, V, V, V, V, I, P(I), I, I, I, I, I, F, V, V, V, V, SZ, V]
             lib.ctx_attn_window_workspace_size.argtypes = [I] * 10
             lib.ctx_attn_window_workspace_size.restype = SZ
-            lib.ctx_attn_decode.argtypes = [T, T, T, V, I, I, I, F, T, V, V, SZ, V]
+            lib.ctx_attn_decode.argtypes = [V, V, V, V, I, I, I, F, V, V, V, SZ, V]
             lib.ctx_attn_decode_workspace_size.argtypes = [I] * 8
             lib.ctx_attn_decode_workspace_size.restype = SZ
-            R = P(_Rope)
-            lib.ctx_rope_fwd.argtypes = [T, T, R, I, I, T, T, V]
-            lib.ctx_rope_bwd.argtypes = [T, T, R, I, I, T, T, V]
-            lib.ctx_qk_norm_rope_fwd.argtypes = [T, T, V, V, I, F, R, I, I, T, T, V]
-            lib.ctx_qk_norm_rope_bwd.argtypes = [T, T, T, T, V, V, I, F, R, I, I, T, T, V, V, V, SZ, V]
+            lib.ctx_rope_fwd.argtypes = [V, V, V, I, I, V, V, V]
+            lib.ctx_rope_bwd.argtypes = [V, V, V, I, I, V, V, V]
+            lib.ctx_qk_norm_rope_fwd.argtypes = [V, V, V, V, I, F, V, I, I, V, V, V]
+            lib.ctx_qk_norm_rope_bwd.argtypes = [V, V, V, V, V, V, I, F, V, I, I, V, V, V, V, V, SZ, V]
             lib.ctx_qk_norm_rope_workspace_size.argtypes = [I]
             lib.ctx_qk_norm_rope_workspace_size.restype = SZ
             lib.ctx_status_string.argtypes = [I]
@@ -177,6 +181,67 @@ def _check_inputs(named, device, lse=None, lse_shape=None):
             raise ValueError(f"{name}: tensor must be on a CUDA device")
         if t.device != device:
             raise ValueError(f"{name}: on {t.device}, the other tensors are on {device}")
+
+
+# ctx_tensor_t and ctx_rope_t in the C compiler's layout.  Short calls (one new
+# token) are bound by the host: a packed descriptor costs a fraction of a
+# ctypes structure.
+_PACK = struct.Struct("P7q").pack
+_PACK_ROPE = struct.Struct("P3i4ifP4q").pack
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes `device` current for a launch when it is not."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _raw_stream(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)  # of torch.cuda.current_stream, without the object
+
+
+def _packed(t, name, dtype, device):
+    """ctx_tensor_t of a logical [B,S,H,D] tensor of this type and device."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 4:
+        raise ValueError(f"{name}: expected a logical [B,S,H,D] tensor, got {len(shape)} dims")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: dtype must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: tensor must be on a CUDA device")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the other tensors are on {device}")
+    if stride[3] != 1:
+        raise ValueError(f"{name}: the D dimension must be contiguous")
+    return _PACK(t.data_ptr(), *shape, *stride[:3])
+
+
+def _result(given, name, like, heads=None):
+    """(tensor, descriptor) of a result: the one given, or a new one of
+    `like`'s type, storage order and shape (with `heads` heads)."""
+    if given is not None:
+        return given, _packed(given, name, like.dtype, like.device)
+    B, S, H, D = like.shape
+    H = heads or H
+    if like.stride(0) >= like.stride(1):  # [B,S,H,D] storage
+        t = torch.empty((B, S, H, D), dtype=like.dtype, device=like.device)
+        return t, _PACK(t.data_ptr(), B, S, H, D, S * H * D, H * D, D)
+    t = torch.empty((S, B, H, D), dtype=like.dtype, device=like.device).permute(1, 0, 2, 3)
+    return t, _PACK(t.data_ptr(), B, S, H, D, H * D, B * H * D, D)
+
+
+def _lse(given, B, H, S, device):
+    if given is None:
+        return torch.empty((B, H, S), dtype=torch.float32, device=device)
+    if (given.dtype != torch.float32 or tuple(given.shape) != (B, H, S) or not given.is_contiguous()
+            or given.device != device):
+        raise ValueError(f"lse: expected a contiguous float32 tensor of shape {(B, H, S)} on {device}, "
+                         f"got {given.dtype} {tuple(given.shape)} on {given.device}")
+    return given
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _stream(t: torch.Tensor):
@@ -299,18 +364,14 @@ def attn_window_fwd(q, k, v, P, window, sinks=0, chunk_offsets=None, causal=Fals
     .. i + right (-1: unlimited; causal: nothing after i), and the first
     ``sinks`` keys of the sequence.  A causal window of W tokens, the query's
     own among them, is (W - 1, 0)."""
-    lib = load_library()
-    named = [("q", q), ("k", k), ("v", v)] + ([("out", out)] if out is not None else [])
-    _check_types(named)
-    B, S, Hq, D = q.shape
-    _check_inputs(named, q.device, lse, (B, Hq, S))
+    lib, dev, bf = load_library(), q.device, torch.bfloat16
     left, right, sinks = _window(window, sinks)
-    out = _like_layout(q, Hq) if out is None else out
-    lse = torch.empty(B, Hq, S, dtype=torch.float32, device=q.device) if lse is None else lse
-    with _on(q.device):
-        rc = lib.ctx_attn_window_fwd(ctypes.byref(_desc(q)), ctypes.byref(_desc(k)), ctypes.byref(_desc(v)), P,
-                                     _offsets(P, chunk_offsets), LAYOUT_BSHD, int(causal), left, right, sinks,
-                                     float(scale) if scale else 0.0, ctypes.byref(_desc(out)), _ptr(lse), _stream(q))
+    dq, dk, dv = _packed(q, "q", bf, dev), _packed(k, "k", bf, dev), _packed(v, "v", bf, dev)
+    out, do = _result(out, "out", q)
+    lse = _lse(lse, q.shape[0], q.shape[2], q.shape[1], dev)
+    with _on(dev):
+        rc = lib.ctx_attn_window_fwd(dq, dk, dv, P, _offsets(P, chunk_offsets), LAYOUT_BSHD, int(causal), left, right,
+                                     sinks, float(scale) if scale else 0.0, do, lse.data_ptr(), _raw_stream(dev))
     _check(rc, "ctx_attn_window_fwd")
     return out, lse
 
@@ -318,25 +379,18 @@ def attn_window_fwd(q, k, v, P, window, sinks=0, chunk_offsets=None, causal=Fals
 def attn_window_bwd(q, k, v, out, lse, dout, P, window, sinks=0, chunk_offsets=None, causal=False, scale=None,
                     dq=None, dk=None, dv=None, workspace=None):
     """Gradients through ``attn_window_fwd`` -> (dq, dk, dv) bf16, stored like q / k."""
-    lib = load_library()
-    named = [("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout)]
-    named += [(n, t) for n, t in (("dq", dq), ("dk", dk), ("dv", dv)) if t is not None]
-    _check_types(named)
-    B, S, Hq, D = q.shape
-    Hkv = k.shape[2]
-    _check_inputs(named, q.device, lse, (B, Hq, S))
+    lib, dev, bf = load_library(), q.device, torch.bfloat16
     left, right, sinks = _window(window, sinks)
-    dq = _like_layout(q, Hq) if dq is None else dq
-    dk = _like_layout(k, Hkv) if dk is None else dk
-    dv = _like_layout(k, Hkv) if dv is None else dv
-    nbytes = lib.ctx_attn_window_workspace_size(B, S, Hq, Hkv, D, P, int(causal), left, right, sinks)
-    ws, wsb = _workspace(nbytes, q.device, workspace)
-    with _on(q.device):
-        rc = lib.ctx_attn_window_bwd(ctypes.byref(_desc(q)), ctypes.byref(_desc(k)), ctypes.byref(_desc(v)),
-                                     ctypes.byref(_desc(out)), _ptr(lse), ctypes.byref(_desc(dout)), P,
-                                     _offsets(P, chunk_offsets), LAYOUT_BSHD, int(causal), left, right, sinks,
-                                     float(scale) if scale else 0.0, ctypes.byref(_desc(dq)), ctypes.byref(_desc(dk)),
-                                     ctypes.byref(_desc(dv)), _ptr(ws), wsb, _stream(q))
+    ins = [_packed(t, n, bf, dev) for n, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout))]
+    B, S, Hq, D = q.shape
+    lse = _lse(lse, B, Hq, S, dev)
+    (dq, pq), (dk, pk), (dv, pv) = _result(dq, "dq", q), _result(dk, "dk", k), _result(dv, "dv", k)
+    with _on(dev):
+        nbytes = lib.ctx_attn_window_workspace_size(B, S, Hq, k.shape[2], D, P, int(causal), left, right, sinks)
+        ws, wsb = _workspace(nbytes, dev, workspace)
+        rc = lib.ctx_attn_window_bwd(*ins[:4], lse.data_ptr(), ins[4], P, _offsets(P, chunk_offsets), LAYOUT_BSHD,
+                                     int(causal), left, right, sinks, float(scale) if scale else 0.0, pq, pk, pv,
+                                     _ptr(ws), wsb, _raw_stream(dev))
     _check(rc, "ctx_attn_window_bwd")
     return dq, dk, dv
 
@@ -356,24 +410,22 @@ def attn_decode(q, k, v, lengths=None, window=-1, sinks=0, scale=None, out=None,
     full).  Query t is at position length - T + t; it sees the keys up to
     itself, of those the last ``window`` before it (-1: all) and the first
     ``sinks``.  A query before its sequence's start gives 0 and -inf."""
-    lib = load_library()
-    named = [("q", q), ("k", k), ("v", v)] + ([("out", out)] if out is not None else [])
-    _check_types(named)
+    lib, dev, bf = load_library(), q.device, torch.bfloat16
+    _, _, sinks = _window((window, 0), sinks)
+    dq, dk, dv = _packed(q, "q", bf, dev), _packed(k, "k", bf, dev), _packed(v, "v", bf, dev)
     B, T, Hq, D = q.shape
-    _check_inputs(named, q.device, lse, (B, Hq, T))
     if lengths is not None and (lengths.dtype != torch.int32 or tuple(lengths.shape) != (B,)
-                                or not lengths.is_contiguous() or lengths.device != q.device):
-        raise ValueError(f"lengths: expected a contiguous int32 tensor of shape {(B,)} on {q.device}, "
+                                or not lengths.is_contiguous() or lengths.device != dev):
+        raise ValueError(f"lengths: expected a contiguous int32 tensor of shape {(B,)} on {dev}, "
                          f"got {lengths.dtype} {tuple(lengths.shape)} on {lengths.device}")
-    left, _, sinks = _window((window, 0), sinks)
-    out = _like_layout(q, Hq) if out is None else out
-    lse = torch.empty(B, Hq, T, dtype=torch.float32, device=q.device) if lse is None else lse
-    with _on(q.device):
+    out, do = _result(out, "out", q)
+    lse = _lse(lse, B, Hq, T, dev)
+    left = min(window, (1 << 31) - 1)
+    with _on(dev):
         ws, wsb = _workspace(lib.ctx_attn_decode_workspace_size(B, T, Hq, k.shape[2], D, k.shape[1], left, sinks),
-                             q.device, workspace)
-        rc = lib.ctx_attn_decode(ctypes.byref(_desc(q)), ctypes.byref(_desc(k)), ctypes.byref(_desc(v)),
-                                 _ptr(lengths), LAYOUT_BSHD, left, sinks, float(scale) if scale else 0.0,
-                                 ctypes.byref(_desc(out)), _ptr(lse), _ptr(ws), wsb, _stream(q))
+                             dev, workspace)
+        rc = lib.ctx_attn_decode(dq, dk, dv, _ptr(lengths), LAYOUT_BSHD, left, sinks, float(scale) if scale else 0.0,
+                                 do, lse.data_ptr(), _ptr(ws), wsb, _raw_stream(dev))
     _check(rc, "ctx_attn_decode")
     return out, lse
 
@@ -429,13 +481,6 @@ def exchanged_view(y, S, layout):
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
-def _on(device):
-    """Makes `device` current for a launch when it is not."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
 @dataclass(frozen=True)
 class RopeTable:
     """Frequencies of a rotary embedding, laid out once (``rope_table``)."""
@@ -444,6 +489,12 @@ class RopeTable:
     interleaved: bool
     sections: tuple      # pairs per position axis
     magnitude: float
+
+    @functools.cached_property
+    def _head(self):
+        """The leading fields of ctx_rope_t."""
+        return (self.turns.data_ptr(), self.rot_dim, int(self.interleaved), len(self.sections),
+                *self.sections, *[0] * (4 - len(self.sections)), self.magnitude)
 
 
 def rope_table(rot_dim, theta=10000.0, interleaved=False, sections=None, scaling="none", factor=1.0,
@@ -510,89 +561,57 @@ def rope_table(rot_dim, theta=10000.0, interleaved=False, sections=None, scaling
 
 
 def _rope_desc(table, positions, offset, B, S, device):
+    """ctx_rope_t of a call (None without a table)."""
     if table is None:
         if positions is not None:
             raise ValueError("positions given without a table")
         return None
     if table.turns.device != device:
         raise ValueError(f"table: on {table.turns.device}, the tensors are on {device}")
-    r = _Rope(table.turns.data_ptr(), table.rot_dim, int(table.interleaved), len(table.sections),
-              (ctypes.c_int * 4)(*table.sections), table.magnitude, None, 0, 0, 0, int(offset))
+    axes = len(table.sections)
     if positions is None:
-        if len(table.sections) > 1:
+        if axes > 1:
             raise ValueError("a table with several position axes needs positions")
-        return r
+        return _PACK_ROPE(*table._head, 0, 0, 0, 0, offset)
     if positions.dtype != torch.int64 or positions.device != device:
         raise ValueError(f"positions: expected int64 on {device}, got {positions.dtype} on {positions.device}")
-    p = positions
-    if len(table.sections) > 1:
-        if p.dim() < 2 or p.shape[-1] != len(table.sections):
-            raise ValueError(f"positions: expected [S, {len(table.sections)}] or [B, S, {len(table.sections)}], "
-                             f"got {tuple(p.shape)}")
-        r.pos_stride_axis = p.stride(-1)
-        p = p.select(-1, 0)
-    if p.dim() == 1 and p.shape[0] == S:
-        r.pos_stride_s = p.stride(0)
-    elif p.dim() == 2 and p.shape[0] in (1, B) and p.shape[1] == S:
-        r.pos_stride_b, r.pos_stride_s = (0 if p.shape[0] == 1 else p.stride(0)), p.stride(1)
+    shape, stride = positions.shape, positions.stride()
+    sa = 0
+    if axes > 1:
+        if len(shape) < 2 or shape[-1] != axes:
+            raise ValueError(f"positions: expected [S, {axes}] or [B, S, {axes}], got {tuple(shape)}")
+        shape, stride, sa = shape[:-1], stride[:-1], stride[-1]
+    if len(shape) == 1 and shape[0] == S:
+        sb, ss = 0, stride[0]
+    elif len(shape) == 2 and shape[0] in (1, B) and shape[1] == S:
+        sb, ss = (0 if shape[0] == 1 else stride[0]), stride[1]
     else:
         raise ValueError(f"positions: {tuple(positions.shape)} does not fit {B} sequences of {S} tokens")
-    r.positions = positions.data_ptr()
-    return r
+    return _PACK_ROPE(*table._head, positions.data_ptr(), sb, ss, sa, offset)
 
 
-def _any_desc(t, name):
-    B, S, H, D = t.shape
-    if t.stride(3) != 1:
-        raise ValueError(f"{name}: the D dimension must be contiguous")
-    return _Tensor(t.data_ptr(), B, S, H, D, t.stride(0), t.stride(1), t.stride(2))
-
-
-def _check_rows(named):
-    """Tensors of one rotary / norm call: ranks, one element type, one device,
-    and the shapes of each side (q's, then k's)."""
-    first = named[0][1]
-    for name, t in named:
-        if t.dim() != 4:
-            raise ValueError(f"{name}: expected a logical [B,S,H,D] tensor, got {t.dim()} dims")
-        if t.dtype not in _DTYPES or t.dtype != first.dtype:
-            raise ValueError(f"{name}: dtype must be bfloat16, float16 or float32, the same for all; got {t.dtype}")
-        if not t.is_cuda or t.device != first.device:
-            raise ValueError(f"{name}: on {t.device}; every tensor must be on one CUDA device")
-        if (t.shape[0], t.shape[1], t.shape[3]) != (first.shape[0], first.shape[1], first.shape[3]):
-            raise ValueError(f"{name}: shape {tuple(t.shape)} does not go with {tuple(first.shape)}")
-
-
-def _rows_like(t):
-    B, S, H, D = t.shape
-    if t.stride(0) >= t.stride(1):
-        return torch.empty(B, S, H, D, dtype=t.dtype, device=t.device)
-    return torch.empty(S, B, H, D, dtype=t.dtype, device=t.device).permute(1, 0, 2, 3)
-
-
-def _ref(t, name):
-    return None if t is None else ctypes.byref(_any_desc(t, name))
-
-
-def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
-
-
-def _given(*named):
-    return [(n, t) for n, t in named if t is not None]
+def _row_type(t, name):
+    if t.dim() != 4:
+        raise ValueError(f"{name}: expected a logical [B,S,H,D] tensor, got {t.dim()} dims")
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
+        raise ValueError(f"{name}: dtype must be bfloat16, float16 or float32, got {t.dtype}")
+    return dtype
 
 
 def _rotate(entry, names, a, b, table, positions, offset, a_out, b_out):
     lib = load_library()
     if table is None:
         raise ValueError("table: a RopeTable is required")
-    _check_rows(_given((names[0], a), (names[1], b), (names[2], a_out), (names[3], b_out)))
-    rope = _rope_desc(table, positions, offset, a.shape[0], a.shape[1], a.device)
-    a_out = _rows_like(a) if a_out is None else a_out
-    b_out = _rows_like(b) if b_out is None and b is not None else b_out
-    with _on(a.device):
-        rc = getattr(lib, entry)(_ref(a, names[0]), _ref(b, names[1]), ctypes.byref(rope), _DTYPES[a.dtype],
-                                 LAYOUT_BSHD, _ref(a_out, names[2]), _ref(b_out, names[3]), _stream(a))
+    dtype, dev, dt = a.dtype, a.device, _row_type(a, names[0])
+    pa, pb = _packed(a, names[0], dtype, dev), None if b is None else _packed(b, names[1], dtype, dev)
+    rope = _rope_desc(table, positions, offset, a.shape[0], a.shape[1], dev)
+    a_out, qa = _result(a_out, names[2], a)
+    qb = None
+    if b is not None:
+        b_out, qb = _result(b_out, names[3], b)
+    with _on(dev):
+        rc = getattr(lib, entry)(pa, pb, rope, dt, LAYOUT_BSHD, qa, qb, _raw_stream(dev))
     _check(rc, entry)
     return a_out, b_out
 
@@ -612,15 +631,17 @@ def rope_bwd(dq_out, dk_out, table, positions=None, offset=0, dq=None, dk=None):
     return _rotate("ctx_rope_bwd", ("dq_out", "dk_out", "dq", "dk"), dq_out, dk_out, table, positions, offset, dq, dk)
 
 
-def _check_weights(named, D, device):
+def _weight_type(wq, wk, D, device):
     dt = None
-    for name, w in named:
-        if tuple(w.shape) != (D,) or not w.is_contiguous() or w.device != device or w.dtype not in _DTYPES:
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is None:
+            continue
+        if w.shape != (D,) or not w.is_contiguous() or w.device != device or w.dtype not in _DTYPES:
             raise ValueError(f"{name}: expected a contiguous [{D}] tensor on {device}, got {w.dtype} {tuple(w.shape)}")
         if dt is not None and w.dtype != dt:
             raise ValueError(f"{name}: both weights must have one dtype")
         dt = w.dtype
-    return _DTYPES[dt] if dt is not None else 2
+    return 2 if dt is None else _DTYPES[dt]
 
 
 def qk_norm_rope_fwd(q, k, wq, wk, table, positions=None, offset=0, eps=1e-6, q_out=None, k_out=None):
@@ -630,15 +651,17 @@ def qk_norm_rope_fwd(q, k, wq, wk, table, positions=None, offset=0, eps=1e-6, q_
     wq, wk: [D] weights or None (ones); table None: the norm alone; the other
     arguments as in ``rope_fwd``."""
     lib = load_library()
-    _check_rows(_given(("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)))
-    wt = _check_weights(_given(("wq", wq), ("wk", wk)), q.shape[3], q.device)
-    rope = _rope_desc(table, positions, offset, q.shape[0], q.shape[1], q.device)
-    q_out = _rows_like(q) if q_out is None else q_out
-    k_out = _rows_like(k) if k_out is None and k is not None else k_out
-    with _on(q.device):
-        rc = lib.ctx_qk_norm_rope_fwd(_ref(q, "q"), _ref(k, "k"), _ptr(wq), _ptr(wk), wt, float(eps),
-                                      None if rope is None else ctypes.byref(rope), _DTYPES[q.dtype], LAYOUT_BSHD,
-                                      _ref(q_out, "q_out"), _ref(k_out, "k_out"), _stream(q))
+    dtype, dev, dt = q.dtype, q.device, _row_type(q, "q")
+    pq, pk = _packed(q, "q", dtype, dev), None if k is None else _packed(k, "k", dtype, dev)
+    wt = _weight_type(wq, wk, q.shape[3], dev)
+    rope = _rope_desc(table, positions, offset, q.shape[0], q.shape[1], dev)
+    q_out, oq = _result(q_out, "q_out", q)
+    ok = None
+    if k is not None:
+        k_out, ok = _result(k_out, "k_out", k)
+    with _on(dev):
+        rc = lib.ctx_qk_norm_rope_fwd(pq, pk, _ptr(wq), _ptr(wk), wt, eps, rope, dt, LAYOUT_BSHD, oq, ok,
+                                      _raw_stream(dev))
     _check(rc, "ctx_qk_norm_rope_fwd")
     return q_out, k_out
 
@@ -652,25 +675,28 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, table, positions=None, offset
     lib = load_library()
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out go together")
-    _check_rows(_given(("q", q), ("dq_out", dq_out), ("k", k), ("dk_out", dk_out), ("dq", dq), ("dk", dk)))
-    D, dev = q.shape[3], q.device
-    wt = _check_weights(_given(("wq", wq), ("wk", wk)), D, dev)
+    dtype, dev, dt = q.dtype, q.device, _row_type(q, "q")
+    pq, pg = _packed(q, "q", dtype, dev), _packed(dq_out, "dq_out", dtype, dev)
+    pk = ph = ok = None
+    if k is not None:
+        pk, ph = _packed(k, "k", dtype, dev), _packed(dk_out, "dk_out", dtype, dev)
+    D = q.shape[3]
+    wt = _weight_type(wq, wk, D, dev)
     for name, g, w in (("dwq", dwq, wq), ("dwk", dwk, wk)):
         if g is not None and (w is None or g.dtype != torch.float32 or tuple(g.shape) != (D,)
                               or not g.is_contiguous() or g.device != dev):
             raise ValueError(f"{name}: expected a contiguous float32 [{D}] tensor on {dev}, beside its weight")
     rope = _rope_desc(table, positions, offset, q.shape[0], q.shape[1], dev)
-    dq = _rows_like(q) if dq is None else dq
-    dk = _rows_like(k) if dk is None and k is not None else dk
+    dq, oq = _result(dq, "dq", q)
+    if k is not None:
+        dk, ok = _result(dk, "dk", k)
     dwq = torch.empty(D, dtype=torch.float32, device=dev) if dwq is None and wq is not None else dwq
     dwk = torch.empty(D, dtype=torch.float32, device=dev) if dwk is None and wk is not None else dwk
     need = lib.ctx_qk_norm_rope_workspace_size(D) if dwq is not None or dwk is not None else 0
     ws, wsb = _workspace(need, dev, workspace)
     with _on(dev):
-        rc = lib.ctx_qk_norm_rope_bwd(_ref(dq_out, "dq_out"), _ref(dk_out, "dk_out"), _ref(q, "q"), _ref(k, "k"),
-                                      _ptr(wq), _ptr(wk), wt, float(eps), None if rope is None else ctypes.byref(rope),
-                                      _DTYPES[q.dtype], LAYOUT_BSHD, _ref(dq, "dq"), _ref(dk, "dk"), _ptr(dwq),
-                                      _ptr(dwk), _ptr(ws), wsb, _stream(q))
+        rc = lib.ctx_qk_norm_rope_bwd(pg, ph, pq, pk, _ptr(wq), _ptr(wk), wt, eps, rope, dt, LAYOUT_BSHD, oq, ok,
+                                      _ptr(dwq), _ptr(dwk), _ptr(ws), wsb, _raw_stream(dev))
     _check(rc, "ctx_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 

@@ -299,7 +299,7 @@ def test_refusals_on_the_gpu():
     table = ctx.rope_table(64)
     with pytest.raises(ValueError):
         ctx.rope_fwd(q, q.float(), table)
-    with pytest.raises(ValueError):
+    with pytest.raises(ctx.CtxError):
         ctx.rope_fwd(q, q[:, :2], table)
     with pytest.raises(ValueError):
         ctx.rope_fwd(q, None, table, positions=torch.zeros(4, dtype=torch.int32, device="cuda"))
