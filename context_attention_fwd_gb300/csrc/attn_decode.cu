@@ -14,8 +14,8 @@
 //     read once per group, not once per query head;
 //   * the keys that some row sees are numbered without gaps, v = 0 .. n - 1
 //     (the sinks, then the window), and cut over `splits` CTAs and then over
-//     the CTA's four warps in tiles of kTileKeys.  Every warp streams its own
-//     tiles through its own ring of cp.async stages and keeps its own (m, l,
+//     the CTA's four warps in tiles of 8 KB.  Every warp streams its own
+//     tiles through its own ring of cp.async slots and keeps its own (m, l,
 //     O), so no barrier stands in the loop; keys past n are zero-filled, never
 //     read;
 //   * products on the warp-level tensor instruction (m16n8k16): a decode step
@@ -53,14 +53,13 @@ struct DecParams {
 
 template <int D>
 struct DecLayout {
-    static constexpr int KEYS = D == 64 ? 32 : 16;       // keys of a warp's tile
-    static constexpr int STAGES = 3;                     // two CTAs per SM (one for D = 256)
+    static constexpr int KEYS = 4096 / D;                // keys of a warp's tile: 8 KB of K, 8 KB of V
+    static constexpr int SLOTS = 3;                      // of 8 KB, K and V tiles in turn; two CTAs per SM
     static constexpr uint32_t ROW = D * 2;               // bytes
-    static constexpr uint32_t HALF = KEYS * ROW;         // K or V of a stage
-    static constexpr uint32_t STAGE = 2 * HALF;
+    static constexpr uint32_t SLOT = KEYS * ROW;
     static constexpr uint32_t OFF_Q = 0;                 // 16 x D bf16
     static constexpr uint32_t OFF_RING = kRows * ROW;
-    static constexpr uint32_t SMEM = OFF_RING + kDecWarps * STAGES * STAGE;
+    static constexpr uint32_t SMEM = OFF_RING + kDecWarps * SLOTS * SLOT;
     static_assert(kDecWarps * kRows * (D + 4) * 4 + kDecWarps * kRows * 8 <= SMEM, "merge buffers reuse the ring");
 };
 
@@ -105,9 +104,10 @@ __device__ __forceinline__ DecSpan dec_span(const DecParams& p, int b) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __grid_constant__ DecParams p) {
+__global__ void __launch_bounds__(32 * kDecWarps, 2) attn_decode_kernel(const __grid_constant__ DecParams p) {
     using L = DecLayout<D>;
     constexpr int KEYS = L::KEYS, NT = KEYS / 8, CH = D / 8;
+    griddep_launch_dependents();  // decode_merge_kernel, which waits for this kernel before it reads
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int warp = warp_id(), lane = lane_id();
@@ -127,29 +127,46 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
     }
     cp_async_commit();
 
-    const uint32_t ring = sbase + L::OFF_RING + warp * L::STAGES * L::STAGE;
+    const uint32_t ring = sbase + L::OFF_RING + warp * L::SLOTS * L::SLOT;
     const __nv_bfloat16* kb = p.k + b * p.k_sb + hk * p.k_sh;
     const __nv_bfloat16* vb = p.v + b * p.v_sb + hk * p.v_sh;
-    // this warp's tiles: t0 + warp, t0 + warp + 4, ...
-    auto load = [&](int tile, int stage) {
-        const uint32_t ks = ring + stage * L::STAGE, vs = ks + L::HALF;
+    // This warp's tiles are t0 + warp, t0 + warp + 4, ..; load n is the K (n
+    // even) or V tile of the n / 2-th of them, and goes to slot n mod 3.  A
+    // thread copies chunk lc of rows lr, lr + kStep, ..; kStep divides 8, so
+    // the row's part of the swizzle is an exclusive or with a constant.
+    constexpr int kStep = 32 / CH;
+    const int lr = lane / CH, lc = lane % CH;
+    const uint32_t dst0 = lr * L::ROW + ((lc ^ lr) << 4);
+    auto load = [&](int n, int slot) {
+        const int tile = t0 + warp + (n >> 1) * kDecWarps;
         if (tile < t1) {
+            const __nv_bfloat16* base = ((n & 1) ? vb : kb) + lc * 8;
+            const int64_t ss = (n & 1) ? p.v_ss : p.k_ss;
+            const uint32_t dst = ring + slot * L::SLOT;
+            const int v0 = tile * KEYS;
+            if (v0 >= sp.ns && v0 + KEYS <= sp.n) {  // whole, past the sinks: consecutive rows
+                const __nv_bfloat16* src = base + (v0 + sp.shift + lr) * ss;
 #pragma unroll
-            for (int i = 0; i < KEYS * CH / 32; ++i) {
-                const int idx = i * 32 + lane, r = idx / CH, c = idx % CH;
-                const int v = tile * KEYS + r;
-                const bool on = v < sp.n;
-                const int64_t key = on ? (v < sp.ns ? v : v + sp.shift) : 0;
-                cp_async16(ks + dec_off<D>(r, c), kb + key * p.k_ss + c * 8, on);
-                cp_async16(vs + dec_off<D>(r, c), vb + key * p.v_ss + c * 8, on);
+                for (int i = 0; i < KEYS / kStep; ++i) {
+                    cp_async16(dst + (dst0 ^ (((i * kStep) & 7) << 4)) + i * kStep * L::ROW, src, true);
+                    src += kStep * ss;
+                }
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < KEYS / kStep; ++i) {
+                    const int v = v0 + i * kStep + lr;
+                    const bool on = v < sp.n;
+                    const int64_t key = on ? (v < sp.ns ? v : v + sp.shift) : 0;
+                    cp_async16(dst + (dst0 ^ (((i * kStep) & 7) << 4)) + i * kStep * L::ROW, base + key * ss, on);
+                }
             }
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < L::STAGES - 1; ++i) load(t0 + warp + i * kDecWarps, i);
+    for (int i = 0; i < L::SLOTS; ++i) load(i, i);
 
-    cp_async_wait<L::STAGES - 1>();
+    cp_async_wait<L::SLOTS>();
     __syncthreads();
     uint32_t qf[D == 256 ? 1 : D / 16][4];  // D = 256 reads them again for every tile: the registers hold O
     const uint32_t q_addr = sbase + L::OFF_Q;
@@ -170,11 +187,12 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-    int stage = 0;
+    int slot = 0, n_load = L::SLOTS;
+    auto next_slot = [&] { slot = slot + 1 == L::SLOTS ? 0 : slot + 1; };
     for (int tile = t0 + warp; tile < t1; tile += kDecWarps) {
-        cp_async_wait<L::STAGES - 2>();
+        cp_async_wait<L::SLOTS - 1>();
         __syncwarp();
-        const uint32_t ks = ring + stage * L::STAGE, vs = ks + L::HALF;
+        const uint32_t ks = ring + slot * L::SLOT;
         float s[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
@@ -191,6 +209,9 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
                 mma16816(s[n + 1], a, kf[2], kf[3]);
             }
         }
+        __syncwarp();  // every thread has read the K tile
+        load(n_load++, slot);
+        next_slot();
         // with one token every loaded key is visible to every row
         const int v0 = tile * KEYS;
         if (p.T > 1 || v0 + KEYS > sp.n) {
@@ -232,6 +253,9 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
             o[i][2] *= alpha[1];
             o[i][3] *= alpha[1];
         }
+        cp_async_wait<L::SLOTS - 1>();
+        __syncwarp();
+        const uint32_t vs = ring + slot * L::SLOT;
 #pragma unroll
         for (int kk = 0; kk < KEYS / 16; ++kk) {
             const uint32_t a[4] = {pack_bf16x2(s[2 * kk][0], s[2 * kk][1]), pack_bf16x2(s[2 * kk][2], s[2 * kk][3]),
@@ -245,9 +269,9 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
                 mma16816(o[2 * i + 1], a, vf[2], vf[3]);
             }
         }
-        __syncwarp();  // the stage just read is the next one written
-        load(tile + (L::STAGES - 1) * kDecWarps, (stage + L::STAGES - 1) % L::STAGES);
-        stage = (stage + 1) % L::STAGES;
+        __syncwarp();  // every thread has read the V tile
+        load(n_load++, slot);
+        next_slot();
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -305,58 +329,95 @@ __global__ void __launch_bounds__(32 * kDecWarps) attn_decode_kernel(const __gri
     }
 }
 
-// out, lse from the splits' states, added in order.  One warp per query row.
+// out, lse of one query row per block from the splits' states.  Every warp
+// holds all the splits' weights (split 32 i + lane in register i), adds the
+// splits warp, warp + 4, .. and the warps' sums are added in order.
 template <int D>
-__global__ void decode_merge_kernel(const __grid_constant__ DecParams p) {
+__global__ void __launch_bounds__(32 * kDecWarps) decode_merge_kernel(const __grid_constant__ DecParams p) {
     griddep_wait();  // the previous kernel in the stream is complete (launch_kernel)
-    const int64_t nrows = (int64_t)p.B * p.Hkv * p.T * p.G;
-    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
-    if (i >= nrows) return;
-    const int lane = lane_id(), per = p.T * p.G;
-    const int rr = (int)(i % per);
-    const int64_t bh = i / per;
+    constexpr int N = D / 32;
+    __shared__ float sm[kDecWarps][D];
+    const int lane = lane_id(), warp = warp_id(), per = p.T * p.G;
+    const int rr = (int)(blockIdx.x % per);
+    const int64_t bh = blockIdx.x / per;
     const int hk = (int)(bh % p.Hkv), b = (int)(bh / p.Hkv);
     const int64_t stride = (int64_t)p.B * p.Hkv * p.row_blocks * kRows;
     const int64_t row = bh * p.row_blocks * kRows + rr;
-    float mm = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) mm = fmaxf(mm, p.part_ml[s * stride + row].x);
+    float f[kMaxSplits / 32], ll = 0.f, mm = -INFINITY;
+    float2 ml[kMaxSplits / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / 32; ++i) {
+        const int s = 32 * i + lane;
+        ml[i] = s < p.splits ? p.part_ml[s * stride + row] : make_float2(-INFINITY, 0.f);
+        mm = fmaxf(mm, ml[i].x);
+    }
     for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
     const float ref = mm == -INFINITY ? 0.f : mm;
-    constexpr int N = D / 32;
-    float acc[N], ll = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / 32; ++i) {
+        f[i] = ex2(ml[i].x - ref);
+        ll = fmaf(ml[i].y, f[i], ll);
+    }
+    for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
+    float acc[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) acc[k] = 0.f;
-    for (int s = 0; s < p.splits; ++s) {
-        const float2 ml = p.part_ml[s * stride + row];
-        const float f = ex2(ml.x - ref);
-        ll = fmaf(ml.y, f, ll);
-        const float* src = p.part_o + (s * stride + row) * D + lane * N;
 #pragma unroll
-        for (int k = 0; k < N; ++k) acc[k] = fmaf(src[k], f, acc[k]);
+    for (int i = 0; i < kMaxSplits / 32; ++i) {
+        if (32 * i >= p.splits) break;
+#pragma unroll
+        for (int e = 0; e < 32; e += kDecWarps) {
+            const int s = 32 * i + e + warp;
+            const float w = __shfl_sync(0xffffffffu, f[i], e + warp);
+            if (s < p.splits) {
+                const float* src = p.part_o + (s * stride + row) * D + lane * N;
+                float x[N];
+                if constexpr (N == 2) {
+                    *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < N; k += 4) *reinterpret_cast<float4*>(x + k) = *reinterpret_cast<const float4*>(src + k);
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k) acc[k] = fmaf(x[k], w, acc[k]);
+            }
+        }
     }
+#pragma unroll
+    for (int k = 0; k < N; ++k) sm[warp][lane * N + k] = acc[k];
+    __syncthreads();
     const int t = rr / p.G, h = hk * p.G + rr % p.G;
     const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
-    __nv_bfloat16* dst = p.out + b * p.o_sb + t * p.o_ss + h * p.o_sh + lane * N;
+    __nv_bfloat16* dst = p.out + b * p.o_sb + t * p.o_ss + h * p.o_sh;
+    for (int i = threadIdx.x; i < D / 2; i += blockDim.x) {
+        float x = 0.f, y = 0.f;
 #pragma unroll
-    for (int k = 0; k < N; k += 2) *reinterpret_cast<uint32_t*>(dst + k) = pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
-    if (lane == 0)
+        for (int w = 0; w < kDecWarps; ++w) {
+            x += sm[w][2 * i];
+            y += sm[w][2 * i + 1];
+        }
+        *reinterpret_cast<uint32_t*>(dst + 2 * i) = pack_bf16x2(x * inv, y * inv);
+    }
+    if (threadIdx.x == 0)
         p.lse[((int64_t)b * p.Hq + h) * p.T + t] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
 }
 
-// Splits of a call: enough CTAs to fill the SMs, no more than there are tiles
-// for all four warps of each at the longest length the cache allows.
+// Splits of a call: one CTA per SM, no more than there are tiles for all four
+// warps of each at the longest length the cache allows.  (Two CTAs fit on an
+// SM, but twice the splits cost more in the join than they bring: 47.0
+// against 44.0 us for a 65536-token history of 32/8 heads, D = 128.)
 int plan_splits(int64_t ctas, int D, int cap, int T, int left, int sinks) {
     int64_t span = cap;
     if (left >= 0) span = std::min(span, (int64_t)left + T + sinks);
-    const int keys = (D == 64 ? 32 : 16) * kDecWarps;
+    const int keys = 4096 / D * kDecWarps;
     const int64_t most = std::min<int64_t>(kMaxSplits, (span + keys - 1) / keys);
-    const int64_t want = (D == 256 ? 1LL : 2LL) * num_sms() / ctas;
+    const int64_t want = num_sms() / ctas;
     return (int)std::max<int64_t>(1, std::min(want, most));
 }
 
 bool decode_sizes_ok(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t cap) {
     return B >= 1 && T >= 1 && Hq >= 1 && Hkv >= 1 && cap >= 1 && Hq % Hkv == 0 && B <= 65535 && T <= 65535 &&
-           Hq <= 65535 && cap <= INT32_MAX && Hkv * ((T * (Hq / Hkv) + kRows - 1) / kRows) <= 65535;
+           Hq <= 65535 && cap <= INT32_MAX && B * Hq * T <= INT32_MAX && Hkv * ((T * (Hq / Hkv) + kRows - 1) / kRows) <= 65535;
 }
 
 size_t decode_ws_bytes(int B, int T, int Hq, int Hkv, int D, int splits) {
@@ -377,8 +438,8 @@ int launch_decode(const DecParams& p, bool pdl, cudaStream_t s) {
     int rc = launch_status(launch_kernel(false, attn_decode_kernel<D>, dim3(p.splits, p.Hkv * p.row_blocks, p.B),
                                          dim3(32 * kDecWarps), L::SMEM, s, p));
     if (rc || p.splits == 1) return rc;
-    const int64_t rows = (int64_t)p.B * p.Hq * p.T;
-    return launch_status(launch_kernel(pdl, decode_merge_kernel<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, p));
+    return launch_status(launch_kernel(pdl, decode_merge_kernel<D>, dim3((unsigned)((int64_t)p.B * p.Hq * p.T)),
+                                       dim3(32 * kDecWarps), 0, s, p));
 }
 
 }  // namespace
@@ -444,9 +505,17 @@ int ctx_attn_decode(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tens
         fprintf(stderr, "ctx_attn_decode: B=%d T=%d Hq=%d Hkv=%d D=%d capacity=%d window=%d sinks=%d | %d splits, %lld CTAs\n",
                 p.B, p.T, p.Hq, p.Hkv, (int)D, p.cap, p.left, p.sinks, p.splits,
                 (long long)p.splits * p.Hkv * p.row_blocks * p.B);
-    if (D == 64) return launch_decode<64>(p, false, s);
-    if (D == 128) return launch_decode<128>(p, false, s);
-    return launch_decode<256>(p, false, s);
+    // the merge kernel's launch overlaps the first kernel, but not in a stream
+    // that is being captured (replaying a graph removes the gap already)
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+        cudaGetLastError();
+        st = cudaStreamCaptureStatusActive;
+    }
+    const bool pdl = st == cudaStreamCaptureStatusNone;
+    if (D == 64) return launch_decode<64>(p, pdl, s);
+    if (D == 128) return launch_decode<128>(p, pdl, s);
+    return launch_decode<256>(p, pdl, s);
 }
 
 }  // extern "C"
