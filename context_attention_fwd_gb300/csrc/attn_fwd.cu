@@ -89,7 +89,7 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
         if (globaltimer_ns() - t0 > limit_ns) break;
 }
 
-template <int D, bool kPartials, bool kHeadMajor, bool kWindow>
+template <int D, bool kPartials, bool kHeadMajor>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
     griddep_wait();  // the previous kernel in the stream is complete (launch_kernel)
     griddep_launch_dependents();
@@ -116,17 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     const int hk = h / p.group;
     const WalkCfg g{r, P, p.causal, p.allgather,
                     qs0 + (hasB ? kTile : 0) + min(kTile, ct.off[r + 1] - (qs0 + (hasB ? kTile : 0))) - 1};
-    WinKv wk;
-    if constexpr (kWindow) wk = win_kv(ct, p.win, p.S, qs0, g.q_last);
-    const int n_kv = kWindow ? wk.count() : kv_count(ct, g);
-    auto walk_first = [&](KvWalk& w) {
-        if constexpr (kWindow) win_first(ct, wk, w);
-        else kv_first(ct, g, w);
-    };
-    auto walk_next = [&](KvWalk& w) {
-        if constexpr (kWindow) win_next(ct, wk, w);
-        else kv_next(ct, g, w);
-    };
+    const int n_kv = kv_count(ct, g);
     constexpr bool partials = kPartials;
     const WaitCtx wc{&abort_flag, p.status, p.timeout_ns};
 
@@ -167,8 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             bool ok = true;
             const int skip = debug_skip_step(p.debug, n_kv);  // -1 in normal use
             KvWalk w;
-            walk_first(w);
-            for (int j = 0; j < n_kv; ++j, walk_next(w)) {
+            kv_first(ct, g, w);
+            for (int j = 0; j < n_kv; ++j, kv_next(ct, g, w)) {
                 if (j == skip) {  // failure injection: no K, V from step j on
                     ok = false;
                     break;
@@ -233,8 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         __syncwarp();  // park the issuer's warp-mates instead of letting them spin
         float m_ref = -INFINITY, l = 0.f;
         KvWalk w;
-        walk_first(w);
-        for (int j = 0; j < n_kv && ok; ++j, walk_next(w)) {
+        kv_first(ct, g, w);
+        for (int j = 0; j < n_kv && ok; ++j, kv_next(ct, g, w)) {
             const int kv_start = ct.off[w.c] + (w.t - w.t0) * kTile;
             const int kv_len = min(kTile, ct.off[w.c + 1] - kv_start);
             const bool first = partials ? (w.t == w.t0) : (j == 0);
@@ -245,9 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             tc_fence_after();
             uint32_t s[128];
             tmem_ld128_sync(taddr + s_cols, s);
-            if constexpr (kWindow) {
-                mask_window(p.win, q_start, row, kv_start, kv_len, s);
-            } else if (kv_len < kTile || diag) {
+            if (kv_len < kTile || diag) {
 #pragma unroll
                 for (int k = 0; k < 128; ++k)
                     if (k >= lim) s[k] = __float_as_uint(-INFINITY);
@@ -409,31 +397,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     if (warp == 1) tmem_dealloc(tmem, L::TM_COLS);
 }
 
-template <int D, bool kPartials, bool kHeadMajor, bool kWindow>
+template <int D, bool kPartials, bool kHeadMajor>
 int launch_fwd_dpo(const FwdParams& p, cudaStream_t s) {
     using L = FwdLayout<D>;
     static OncePerDevice attr;
     if (!attr.run([] {
-            return cudaFuncSetAttribute(attn_fwd_kernel<D, kPartials, kHeadMajor, kWindow>,
+            return cudaFuncSetAttribute(attn_fwd_kernel<D, kPartials, kHeadMajor>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) == cudaSuccess;
         }))
         return 4;
-    const cudaError_t e = launch_kernel(p.pdl != 0, attn_fwd_kernel<D, kPartials, kHeadMajor, kWindow>,
+    const cudaError_t e = launch_kernel(p.pdl != 0, attn_fwd_kernel<D, kPartials, kHeadMajor>,
                                         grid_dims(kHeadMajor, p.ct.npairs, p.Hq, p.B), dim3(kThreads), L::SMEM, s, p);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : 4;
 }
 
 template <int D, bool kPartials>
 int launch_fwd_dp(const FwdParams& p, cudaStream_t s) {
-    return p.head_major ? launch_fwd_dpo<D, kPartials, true, false>(p, s)
-                        : launch_fwd_dpo<D, kPartials, false, false>(p, s);
+    return p.head_major ? launch_fwd_dpo<D, kPartials, true>(p, s) : launch_fwd_dpo<D, kPartials, false>(p, s);
 }
 
 // The materialised-partials code path is a separate instantiation so that
 // the default online kernel carries none of its registers.
 template <int D>
 int launch_fwd_d(const FwdParams& p, cudaStream_t s) {
-    if (p.windowed) return launch_fwd_dpo<D, false, false, true>(p, s);
     return p.part_o ? launch_fwd_dp<D, true>(p, s) : launch_fwd_dp<D, false>(p, s);
 }
 
@@ -441,7 +427,7 @@ int launch_fwd_d(const FwdParams& p, cudaStream_t s) {
 
 int attn_fwd_binary_version() {
     cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, attn_fwd_kernel<128, false, false, false>) != cudaSuccess) return -1;
+    if (cudaFuncGetAttributes(&a, attn_fwd_kernel<128, false, false>) != cudaSuccess) return -1;
     return a.binaryVersion;
 }
 

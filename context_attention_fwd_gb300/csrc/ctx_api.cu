@@ -667,10 +667,12 @@ int attn_fwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k
                 name, p.B, p.S, p.Hq, p.Hkv, (int)D, P, p.causal, window_text(win, p.win).s,
                 p.allgather ? "all-gather" : "ring", partials ? 1 : 0,
                 p.ct.ntiles, (long long)fwd_ctas(p.ct, p.B, p.Hq, (int)D),
-                D == 256 ? "attn_fwd256_kernel, one tile per CTA" : "attn_fwd_kernel, two tiles per CTA",
+                D == 256 ? "attn_fwd256_kernel, one tile per CTA"
+                : win    ? "attn_window_kernel, one tile per CTA"
+                         : "attn_fwd_kernel, two tiles per CTA",
                 p.head_major ? "head-major" : "tile-major");
     prof_record(0, 0, s);
-    rc = launch_attn_fwd(p, (int)D, s);
+    rc = win ? launch_attn_window_fwd(p, (int)D, s) : launch_attn_fwd(p, (int)D, s);
     prof_record(0, 1, s);
     if (rc) return rc;
     if (partials) {

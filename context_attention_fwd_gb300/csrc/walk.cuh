@@ -174,6 +174,13 @@ __device__ __forceinline__ void win_next(const ChunkTable& ct, const WinKv& g, K
     }
 }
 
+// The same walk as a step j and its chunk (fewer registers than KvWalk).
+__device__ __forceinline__ int win_tile(const WinKv& g, int j) { return j < g.a ? j : g.b0 + j - g.a; }
+__device__ __forceinline__ int win_chunk(const ChunkTable& ct, int t, int c) {  // chunk of t, not before c
+    while (ct.tile_off[c + 1] <= t) ++c;
+    return c;
+}
+
 // Bits [0, n) of the 32-bit word that holds bits [base, base + 32).
 __device__ __forceinline__ uint32_t bits_below(int n, int base) {
     const int k = n - base;
