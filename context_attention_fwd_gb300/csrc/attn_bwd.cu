@@ -100,7 +100,7 @@ __device__ __forceinline__ void red_add_v4(float* addr, float a, float b, float 
                  : "memory");
 }
 
-// 32 fp32 columns of a partial dK / dV row, summed by sink_reduce_kernel.
+// 32 fp32 columns of a partial dK / dV row, summed by window_reduce_kernel.
 __device__ __forceinline__ void store_part(float* dst, const uint32_t* o) {
     float4* d4 = reinterpret_cast<float4*>(dst);
 #pragma unroll
@@ -123,33 +123,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
     const int warp = warp_id(), lane = lane_id();
     const GridPos gp = grid_pos<kHeadMajor>();
     const WinWork ww = kWindow ? win_work(gp.tile, p.sink_tiles, p.sink_parts) : WinWork{gp.tile, -1};
-    const int kt = ww.kv_tile, hk = gp.head, b = gp.z;
+    const int kt = ww.kv_tile, hk = gp.head, b = kWindow ? gp.z / p.hsplit : gp.z;
+    const int split = kWindow ? gp.z % p.hsplit : 0;  // share of the group's query heads
     const ChunkTable& ct = p.ct;
     const int c = chunk_of_tile(ct, kt);
     const int kv_start = ct.off[c] + (kt - ct.tile_off[c]) * kTile;
     const int kv_len = min(kTile, ct.off[c + 1] - kv_start);
-    const int G = p.group;
+    const int G = kWindow ? p.group / p.hsplit : p.group;  // query heads of this CTA
+    const int h0 = hk * p.group + split * G;
     const auto qw = [&] {
         if constexpr (kWindow) {
             const WinQ q = ww.part < 0 ? win_near_q(ct, p.win, p.S, kv_start, kv_start + kv_len)
                                        : win_part_q(ct, p.win, kt, ww.part, p.sink_per);
-            return WinQWalk{&ct, q, q.t0 < ct.ntiles ? chunk_of_tile(ct, q.t0) : 0, hk * G + G};
+            return WinQWalk{&ct, q, q.t0 < ct.ntiles ? chunk_of_tile(ct, q.t0) : 0, h0 + G};
         } else {
-            return QWalk{&ct, c, p.causal, kv_start, hk * G + G};
+            return QWalk{&ct, c, p.causal, kv_start, h0 + G};
         }
     }();
     const int n_q = qw.count(G);  // query tiles this CTA visits (all heads of the group)
     const WaitCtx wc{&bars.abort_flag, p.status, p.timeout_ns};
     if (kWindow && n_q == 0) return;  // a part past the last query tile
-    // windowed sink tiles: fp32 partial rows of this part, and how many it writes
+    // windowed: fp32 partial rows of this piece (null: it is the only one), and how many it writes
     float* part_row = nullptr;
     int part_rows = 0;
     if constexpr (kWindow) {
-        if (ww.part >= 0 && p.dkv_part) {
-            part_row = p.dkv_part + ((((size_t)ww.part * p.B + b) * p.Hkv + hk) * p.sink_rows + kv_start) * 2 * D;
-            part_rows = win_overlap(qw.q, win_near_q(ct, p.win, p.S, kv_start, kv_start + kv_len))
-                            ? kv_len : min(kv_len, p.win.sinks - kv_start);
-        }
+        part_row = win_part_rows<D>(p, ww, split, b, hk, kv_start);
+        part_rows = ww.part < 0 || win_overlap(qw.q, win_near_q(ct, p.win, p.S, kv_start, kv_start + kv_len))
+                        ? kv_len : min(kv_len, p.win.sinks - kv_start);
     }
 
     if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_bwd_kernel(const __grid_cons
 
     // query-tile walk: ring order from chunk c (causal: tiles entirely
     // above the diagonal are skipped)
-    const QTileIter q0 = qw.first(hk * G);
+    const QTileIter q0 = qw.first(h0);
     auto next = [&](QTileIter& q) { qw.next(q); };
     auto q_first_row = [&](const QTileIter& q) { return qw.first_row(q); };
 
@@ -511,13 +511,13 @@ int launch_bwd_do(const BwdParams& p, cudaStream_t s) {
         return 4;
     const int tiles = kWindow ? win_grid(p.ct.ntiles, p.sink_tiles, p.sink_parts) : p.ct.ntiles;
     const cudaError_t e = launch_kernel(p.pdl != 0, attn_bwd_kernel<D, kHeadMajor, kWindow>,
-                                        grid_dims(kHeadMajor, tiles, p.Hkv, p.B), dim3(kThreads), L::SMEM, s, p);
+                                        grid_dims(kHeadMajor, tiles, p.Hkv, kWindow ? p.B * p.hsplit : p.B), dim3(kThreads), L::SMEM, s, p);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : 4;
 }
 
 template <int D>
 int launch_bwd_d(const BwdParams& p, cudaStream_t s) {
-    if (p.windowed) return launch_bwd_do<D, false, true>(p, s);
+    if (p.windowed) return p.head_major ? launch_bwd_do<D, true, true>(p, s) : launch_bwd_do<D, false, true>(p, s);
     return p.head_major ? launch_bwd_do<D, true, false>(p, s) : launch_bwd_do<D, false, false>(p, s);
 }
 

@@ -538,15 +538,18 @@ __global__ void __launch_bounds__(kB256Threads, 1) attn_bwd256_kernel(const __gr
     const uint32_t tmem = bars.tmem_slot;
     const QTileIter q0 = qw.first(h0);
     // fp32 partial rows of this CTA's (split, b, hk) when the group is split
-    // (or, windowed, of this part of a sink tile's walk, which may only hold sink rows)
-    float* const part_row = !p.dkv_part || (kWindow && ww.part < 0)
-        ? nullptr
-        : p.dkv_part + ((((size_t)((kWindow ? ww.part : split) * p.B + b) * p.Hkv + hk) *
-                         (kWindow ? p.sink_rows : p.S) + kv_start) * 2) * kD + hh * 128;
+    // (windowed: of this piece, which past the window's reach holds sink rows alone)
+    float* part_row;
     int part_rows = kv_len;
     if constexpr (kWindow) {
-        if (part_row && !win_overlap(qw.q, win_near_q(ct, p.win, p.S, kv_start, kv_start + kv_len)))
+        part_row = win_part_rows<kD>(p, ww, split, b, hk, kv_start);
+        if (part_row) part_row += hh * 128;
+        if (ww.part >= 0 && !win_overlap(qw.q, win_near_q(ct, p.win, p.S, kv_start, kv_start + kv_len)))
             part_rows = min(kv_len, p.win.sinks - kv_start);
+    } else {
+        part_row = p.dkv_part
+            ? p.dkv_part + ((((size_t)(split * p.B + b) * p.Hkv + hk) * p.S + kv_start) * 2) * kD + hh * 128
+            : nullptr;
     }
     auto slot_of = [](int n) { return n % L::SLOTS; };
     auto phase_of = [](int n) { return (n / L::SLOTS) & 1; };
@@ -896,11 +899,11 @@ int launch_attn_fwd256(const FwdParams& p, cudaStream_t s) {
 }
 
 int launch_attn_bwd256(const BwdParams& p, cudaStream_t s) {
-    const bool heads_first = p.head_major && !p.windowed;
-    auto kern = p.windowed ? attn_bwd256_kernel<false, true>
+    const bool heads_first = p.head_major;
+    auto kern = p.windowed ? (heads_first ? attn_bwd256_kernel<true, true> : attn_bwd256_kernel<false, true>)
                            : heads_first ? attn_bwd256_kernel<true, false> : attn_bwd256_kernel<false, false>;
-    static OncePerDevice attr[3];
-    if (!attr[p.windowed ? 2 : heads_first ? 1 : 0].run([&] {
+    static OncePerDevice attr[4];
+    if (!attr[(p.windowed ? 2 : 0) + (heads_first ? 1 : 0)].run([&] {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, B256::SMEM) == cudaSuccess;
         }))
         return 4;

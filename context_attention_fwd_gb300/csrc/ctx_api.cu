@@ -4,6 +4,7 @@
 // row statistics (delta = rowsum(dO o O)), the dQ fp32 -> bf16 conversion and
 // the LSE merge of materialised partials.
 #include <math.h>
+#include <stddef.h>
 #include <stdio.h>
 #include <stdlib.h>
 
@@ -184,7 +185,7 @@ __global__ void exchange_kernel(const uint16_t* __restrict__ x, uint16_t* __rest
 // (negated, so the backward adds it in one fused multiply-add).  Slots past
 // a chunk's end get delta 0 and -inf, which makes their probabilities
 // exactly 0 in the backward kernel.  Each thread also zeroes
-// its 8 columns of the row's fp32 dQ accumulator (tile-major
+// eight values of the fp32 dQ accumulator (tile-major
 // [B][Hq][ntiles][D/4][128][4]), which the backward kernel adds into.
 __global__ void bwd_stats_kernel(const __nv_bfloat16* __restrict__ out, int64_t osb, int64_t oss,
                                  int64_t osh, const __nv_bfloat16* __restrict__ dout, int64_t dsb,
@@ -202,11 +203,16 @@ __global__ void bwd_stats_kernel(const __nv_bfloat16* __restrict__ out, int64_t 
     const int64_t sl = in_range ? slot : 0;
     const int rr = (int)(sl % kTile);
     const int64_t bht = sl / kTile;
-    if (in_range) {
-        float* tile = dq_acc + bht * kTile * D;
-        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<float4*>(tile + ((int64_t)(2 * part) * kTile + rr) * 4) = z;
-        *reinterpret_cast<float4*>(tile + ((int64_t)(2 * part + 1) * kTile + rr) * 4) = z;
+    {
+        // zeroed in memory order, whatever rows the block has: its blockDim.x
+        // threads clear two float4 each of consecutive lines
+        float4* z4 = reinterpret_cast<float4*>(dq_acc) + (int64_t)blockIdx.x * blockDim.x * 2;
+        const int64_t end = nslots * (D / 4);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int64_t i = (int64_t)k * blockDim.x + threadIdx.x;
+            if ((int64_t)blockIdx.x * blockDim.x * 2 + i < end) z4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     }
     const int t = (int)(bht % ct.ntiles);
     const int64_t bh = bht / ct.ntiles;
@@ -295,38 +301,49 @@ __global__ void dkv_reduce_kernel(const float* __restrict__ part, int hs, int B,
     *reinterpret_cast<uint4*>(dst) = v;
 }
 
-// Sums of the partial dK / dV rows of the KV tiles that hold sinks (windowed
-// backward): part [sink_parts][B][Hkv][sink_rows][2][D] fp32 (dK unscaled) ->
-// bf16 dk = scale * sum, dv = sum.  A part beyond the window's reach wrote
-// the sink rows alone, one past the last query tile nothing.  One thread per
-// 8 columns; parts are added in order.
-__global__ void sink_reduce_kernel(const __grid_constant__ BwdParams p, int D) {
+// Sums of the partial dK / dV rows of a windowed backward (BwdParams in
+// internal.h): the sink tiles' pieces and, when the query heads of a group are
+// split, every other row's -> bf16 dk = scale * sum, dv = sum.  A piece beyond
+// the window's reach wrote the sink rows alone, one past the last query tile
+// nothing.  One thread per 8 columns; pieces are added in order.
+__global__ void window_reduce_kernel(const __grid_constant__ BwdParams p, int D, int rows) {
     griddep_wait();  // the previous kernel in the stream is complete (launch_kernel)
     griddep_launch_dependents();
     const int g8 = D / 8;
-    const int64_t n = (int64_t)p.B * p.Hkv * p.sink_rows * 2;  // (b, hk, row, which) rows of one part
     const int64_t gt = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (gt >= n * g8) return;
-    const int64_t r = gt / g8;
+    const int64_t r = gt / g8;  // (b, hk, row, which)
+    if (r >= (int64_t)p.B * p.Hkv * rows * 2) return;
     const int k8 = (int)(gt - r * g8);
     const int which = (int)(r & 1);
     const int64_t bhs = r >> 1;
-    const int s = (int)(bhs % p.sink_rows);
-    const int64_t bh = bhs / p.sink_rows;
+    const int s = (int)(bhs % rows);
+    const int64_t bh = bhs / rows;
     const int hk = (int)(bh % p.Hkv), b = (int)(bh / p.Hkv);
-    const int kt = tile_of_row(p.ct, s);
-    const int kv_start = tile_first_row(p.ct, kt);
-    const int kv_end = min(p.ct.off[chunk_of_tile(p.ct, kt) + 1], kv_start + kTile);
-    const WinQ near = win_near_q(p.ct, p.win, p.S, kv_start, kv_end);
+    const bool sink = s < p.sink_rows;
+    const int part_rows = sink ? p.sink_rows : p.S;
+    const int64_t piece = (int64_t)p.B * p.Hkv * part_rows * 2 * D;
+    const float* src = (sink ? p.sink_part : p.dkv_part) + ((bh * part_rows + s) * 2 + which) * D + k8 * 8;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < p.sink_parts; ++i) {
-        const WinQ q = win_part_q(p.ct, p.win, kt, i, p.sink_per);
-        if (q.t0 >= q.t1) break;
-        if (s >= p.win.sinks && !win_overlap(q, near)) continue;
-        const float4* src = reinterpret_cast<const float4*>(p.dkv_part + ((int64_t)i * n + r) * D + k8 * 8);
-        const float4 lo = src[0], hi = src[1];
+    auto add = [&](int64_t i) {
+        const float4* x = reinterpret_cast<const float4*>(src + i * piece);
+        const float4 lo = x[0], hi = x[1];
         acc[0] += lo.x; acc[1] += lo.y; acc[2] += lo.z; acc[3] += lo.w;
         acc[4] += hi.x; acc[5] += hi.y; acc[6] += hi.z; acc[7] += hi.w;
+    };
+    if (sink) {
+        if (!p.sink_part) return;  // one piece, written by its CTA
+        const int kt = tile_of_row(p.ct, s);
+        const int kv_start = tile_first_row(p.ct, kt);
+        const int kv_end = min(p.ct.off[chunk_of_tile(p.ct, kt) + 1], kv_start + kTile);
+        const WinQ near = win_near_q(p.ct, p.win, p.S, kv_start, kv_end);
+        for (int i = 0; i < p.sink_parts; ++i) {
+            const WinQ q = win_part_q(p.ct, p.win, kt, i, p.sink_per);
+            if (q.t0 >= q.t1) break;
+            if (s >= p.win.sinks && !win_overlap(q, near)) continue;
+            for (int e = 0; e < p.hsplit; ++e) add((int64_t)i * p.hsplit + e);
+        }
+    } else {
+        for (int e = 0; e < p.hsplit; ++e) add(e);
     }
     const float f = which == 0 ? p.scale : 1.f;
     uint4 v = make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
@@ -557,39 +574,131 @@ int window_tiles(const Window& w, int ntiles) {
     return n < ntiles ? (int)n : ntiles;
 }
 
-// How the walks of the KV tiles that hold sinks are cut: parts of about the
-// length of the other tiles' walks, eight tiles at least, so that no CTA runs
-// much longer than the rest; at most 64 CTAs over all sink tiles (one each
-// from 64 sink tiles on), which also bounds the partial rows in memory.
-int sink_parts_max(const Window& w, int ntiles) {
-    int n = window_tiles(w, ntiles);
-    if (n < 8) n = 8;
+// How a windowed backward is cut into CTAs: hsplit over the query heads of a
+// group, sink_parts over the long walks of the KV tiles that hold sinks.
+//
+// Their most, which the workspace is sized for and which only grows with the
+// number of tiles: enough head splits to give every SM a CTA; parts down to
+// half the length of the other tiles' walks (eight tiles at least), 64 CTAs
+// over all sink tiles.
+int win_hsplit_cap(int S, int B, int Hq, int Hkv, int D) {
+    const int G = Hq / Hkv, nsm = num_sms();
+    const int64_t base = (int64_t)((S + kTile - 1) / kTile) * Hkv * B * (D == 256 ? 2 : 1);
+    for (int d = 1; d < G; ++d)
+        if (G % d == 0 && base * d >= 2LL * nsm) return d;
+    return G;
+}
+int sink_parts_cap(const Window& w, int ntiles) {
+    const int n = std::max(4, window_tiles(w, ntiles) / 2);
     const int by_length = (ntiles + n - 1) / n, by_count = 64 / ((w.sinks + kTile - 1) / kTile);
     return std::max(1, std::min(by_length, by_count));
 }
 
-void plan_window_bwd(BwdParams* p, int S) {
-    const int ntiles = p->ct.ntiles;
-    p->sink_parts = 1;
-    p->sink_per = ntiles;
-    if (p->win.sinks <= 0) return;
-    p->sink_tiles = tile_of_row(p->ct, p->win.sinks - 1) + 1;
-    const int last = p->sink_tiles - 1, c = chunk_of_tile(p->ct, last);
-    p->sink_rows = std::min(p->ct.off[c + 1], tile_first_row(p->ct, last) + kTile);
-    p->sink_parts = sink_parts_max(p->win, ntiles);
-    p->sink_per = (ntiles + p->sink_parts - 1) / p->sink_parts;
+// Estimated time of a windowed backward in query-tile iterations of one CTA:
+// the CTAs in launch order, each on the first SM that is free, each with its
+// walk and about three iterations to start and end; summing partial rows adds
+// the time of their traffic.
+double win_split_time(const BwdParams& p, int D, int hs, int parts, int per, int head_major, int nsm) {
+    std::vector<double> work;  // of the CTAs of one (head, z), in tile order
+    const int G = p.group / hs;
+    for (int i = 0; i < win_grid(p.ct.ntiles, p.sink_tiles, parts); ++i) {
+        const WinWork w = win_work(i, p.sink_tiles, parts);
+        const int k0 = tile_first_row(p.ct, w.kv_tile);
+        const int k1 = std::min(p.ct.off[chunk_of_tile(p.ct, w.kv_tile) + 1], k0 + kTile);
+        const WinQ q = w.part < 0 ? win_near_q(p.ct, p.win, p.S, k0, k1) : win_part_q(p.ct, p.win, w.kv_tile, w.part, per);
+        work.push_back(q.t1 > q.t0 ? (q.t1 - q.t0) * G + 3.0 : 0.2);
+    }
+    const int64_t other = (int64_t)p.Hkv * p.B * hs * (D == 256 ? 2 : 1);
+    std::vector<double> sm((size_t)nsm, 0.0);  // min-heap of SM finish times
+    auto run = [&](double w) {
+        std::pop_heap(sm.begin(), sm.end(), std::greater<double>());
+        sm.back() += w;
+        std::push_heap(sm.begin(), sm.end(), std::greater<double>());
+    };
+    if (head_major) {
+        for (double w : work)
+            for (int64_t j = 0; j < other; ++j) run(w);
+    } else {
+        for (int64_t j = 0; j < other; ++j)
+            for (double w : work) run(w);
+    }
+    const double span = *std::max_element(sm.begin(), sm.end());
+    // partial rows: D * 8 bytes written and read, against some 3 us an iteration
+    const double rows = (hs > 1 ? (double)hs * p.S : 0.0) + (hs * parts > 1 ? (double)hs * parts * p.sink_rows : 0.0);
+    return span + rows * p.B * p.Hkv * D * 16.0 / 6e12 / 3e-6 + (hs * parts > 1 ? 1.0 : 0.0);
 }
 
+// The cut a call uses: the one of smallest estimated time, among the divisors
+// of the group size and the numbers of parts up to their most (ties to the
+// fewer pieces).  Long calls have CTAs enough: there the heads are not split.  Memoised: the estimate
+// runs on the host.
+void plan_window_bwd(BwdParams* p, int D) {
+    const int nt = p->ct.ntiles, S = p->S;
+    p->hsplit = p->sink_parts = 1;
+    p->sink_tiles = p->sink_rows = 0;
+    p->head_major = 1;
+    if (p->win.sinks > 0) {
+        p->sink_tiles = tile_of_row(p->ct, p->win.sinks - 1) + 1;
+        const int last = p->sink_tiles - 1, c = chunk_of_tile(p->ct, last);
+        p->sink_rows = std::min(p->ct.off[c + 1], tile_first_row(p->ct, last) + kTile);
+    }
+    const int pmax = p->win.sinks > 0 ? sink_parts_cap(p->win, nt) : 1;
+    const int hmax = win_hsplit_cap(S, p->B, p->Hq, p->Hkv, D), nsm = num_sms();
+    const int64_t ctas = (int64_t)nt * p->Hkv * p->B * (D == 256 ? 2 : 1);
+    auto per_of = [&](int parts) { return (nt + parts - 1) / parts; };
+    if (ctas > 4LL * nsm) {
+        // pieces of a quarter of what each SM has to do in all, or of the
+        // other walks' length if that is more
+        const int wt = window_tiles(p->win, nt);
+        const int64_t per = std::max<int64_t>(wt, ctas * wt / (4LL * nsm));
+        p->sink_parts = std::max(1, std::min<int>(pmax, (int)((nt + per - 1) / per)));
+    } else if (pmax > 1 || hmax > 1) {
+        struct Entry {
+            int64_t nt, S, B, Hq, Hkv, D, left, right, sinks, causal, sink_rows, nsm;
+            int hs, parts;
+        };
+        static std::mutex mu;
+        static Entry memo[32];
+        static int n_memo = 0, next_slot = 0;
+        Entry key{nt, S, p->B, p->Hq, p->Hkv, D, p->win.left, p->win.right, p->win.sinks, p->win.causal, p->sink_rows, nsm, 1, 1};
+        std::lock_guard<std::mutex> lock(mu);
+        const Entry* hit = nullptr;
+        for (int i = 0; i < n_memo; ++i)
+            if (!memcmp(&memo[i], &key, offsetof(Entry, hs))) hit = &memo[i];
+        if (!hit) {
+            double best = 0.0;
+            for (int hs = 1; hs <= hmax; ++hs) {
+                if (p->group % hs) continue;
+                for (int parts = 1; parts <= pmax; parts += std::max(1, pmax / 8)) {
+                    const double t = win_split_time(*p, D, hs, parts, per_of(parts), p->head_major, nsm);
+                    if ((hs == 1 && parts == 1) || t < best) best = t, key.hs = hs, key.parts = parts;
+                }
+            }
+            memo[next_slot] = key;
+            hit = &memo[next_slot];
+            next_slot = (next_slot + 1) % 32;
+            if (n_memo < 32) ++n_memo;
+        }
+        p->hsplit = hit->hs;
+        p->sink_parts = hit->parts;
+    }
+    if ((int64_t)p->B * 2 * p->hsplit > 65535) p->hsplit = 1;  // grid limit
+    p->sink_per = per_of(p->sink_parts);
+}
+
+size_t win_part_bytes(int B, int S, int Hq, int Hkv, int D, int hs) {
+    return hs > 1 ? align256((size_t)hs * B * Hkv * S * 2 * D * 4) : 0;
+}
 size_t win_bwd_ws_bytes(int B, int S, int Hq, int Hkv, int D, int P, const Window& w) {
     const size_t slots = (size_t)B * Hq * ntiles_upper(S, P) * kTile;
-    size_t part = 0;
+    const int hs = win_hsplit_cap(S, B, Hq, Hkv, D);
+    size_t part = win_part_bytes(B, S, Hq, Hkv, D, hs);
     if (w.sinks > 0) {
-        // enough for any chunking: sink_parts_max grows with the number of
-        // tiles, and the sink rows end with a tile that starts before the
-        // last sink does
-        const int parts = sink_parts_max(w, (int)ntiles_upper(S, P));
+        // enough for any chunking: the sink rows end with a tile that starts
+        // before the last sink does
+        const int pieces = sink_parts_cap(w, (int)ntiles_upper(S, P)) * hs;
         const size_t rows = std::min((size_t)S, (size_t)w.sinks + kTile);
-        if (parts > 1) part = align256((size_t)parts * B * Hkv * rows * 2 * D * 4);
+        if (pieces > 1) part += align256((size_t)pieces * B * Hkv * rows * 2 * D * 4);
     }
     return align256(slots * 4) * 2 + align256(slots * D * 4) + part;
 }
@@ -720,7 +829,6 @@ int attn_bwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k
     if (win) {
         if ((rc = make_window(*win, (int)S, causal, &p.win))) return rc;
         p.windowed = 1;
-        plan_window_bwd(&p, (int)S);
     }
     const size_t need = win ? win_bwd_ws_bytes((int)B, (int)S, (int)Hq, (int)Hkv, (int)D, P, p.win)
                             : bwd_ws_bytes((int)B, (int)S, (int)Hq, (int)Hkv, (int)D, P);
@@ -733,13 +841,19 @@ int attn_bwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k
     float* dq_acc = reinterpret_cast<float*>(ws + 2 * align256(slots * 4));
     int64_t bwd_ctas = 0;
     if (win) {
-        p.hsplit = 1;
-        bwd_ctas = (int64_t)win_grid(p.ct.ntiles, p.sink_tiles, p.sink_parts) * Hkv * B * (D == 256 ? 2 : 1);
+        p.B = (int)B; p.S = (int)S; p.Hq = (int)Hq; p.Hkv = (int)Hkv;
+        p.group = (int)(Hq / Hkv);
+        plan_window_bwd(&p, (int)D);
+        bwd_ctas = (int64_t)win_grid(p.ct.ntiles, p.sink_tiles, p.sink_parts) * Hkv * B * p.hsplit * (D == 256 ? 2 : 1);
     } else {
         bwd_plan(p.ct, (int)S, (int)B, (int)Hq, (int)Hkv, (int)D, causal ? 1 : 0, &p.hsplit, &p.head_major,
                  &bwd_ctas);
     }
-    p.dkv_part = p.hsplit > 1 || p.sink_parts > 1 ? reinterpret_cast<float*>(ws + 2 * align256(slots * 4) + align256(slots * D * 4))
+    char* const parts = ws + 2 * align256(slots * 4) + align256(slots * D * 4);
+    p.sink_part = p.sink_tiles > 0 && p.hsplit * p.sink_parts > 1
+                      ? reinterpret_cast<float*>(parts + win_part_bytes((int)B, (int)S, (int)Hq, (int)Hkv, (int)D, p.hsplit))
+                      : nullptr;
+    p.dkv_part = p.hsplit > 1 ? reinterpret_cast<float*>(parts)
                               : nullptr;
     if (!make_tmap_bshd(&p.tq, tq.data, B, S, Hq, D, tq.sb, tq.ss, tq.sh, 64, kTile) ||
         !make_tmap_bshd(&p.tk, tk.data, B, S, Hkv, D, tk.sb, tk.ss, tk.sh, 64, kTile) ||
@@ -786,11 +900,12 @@ int attn_bwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k
     rc = launch_attn_bwd(p, (int)D, s);
     prof_record(1, 1, s);
     if (rc) return rc;
-    if (p.dkv_part && win) {
-        const int64_t threads = B * Hkv * p.sink_rows * 2 * (D / 8);
+    if (win && (p.dkv_part || p.sink_part)) {
+        const int rows = p.dkv_part ? (int)S : p.sink_rows;
+        const int64_t threads = B * Hkv * rows * 2 * (D / 8);
         const int blk = 256;
-        rc = launch_status(launch_kernel(p.pdl != 0, sink_reduce_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
-                                         dim3(blk), 0, s, p, (int)D));
+        rc = launch_status(launch_kernel(p.pdl != 0, window_reduce_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
+                                         dim3(blk), 0, s, p, (int)D, rows));
         if (rc) return rc;
     } else if (p.dkv_part) {
         const int64_t threads = B * Hkv * S * 2 * (D / 8);
@@ -898,8 +1013,12 @@ int ctx_attn_window_bwd(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_
                         const ctx_tensor_t* dk, const ctx_tensor_t* dv, void* workspace,
                         size_t workspace_bytes, ctx_stream_t stream) {
     const WindowArgs win{window_left, window_right, sinks};
-    return attn_bwd_call("ctx_attn_window_bwd", q, k, v, out, lse, dout, P, chunk_offsets, layout, causal, &win,
-                         scale, dq, dk, dv, workspace, workspace_bytes, stream);
+    try {
+        return attn_bwd_call("ctx_attn_window_bwd", q, k, v, out, lse, dout, P, chunk_offsets, layout, causal, &win,
+                             scale, dq, dk, dv, workspace, workspace_bytes, stream);
+    } catch (...) {  // host memory of the launch plan's estimate
+        return CTX_ERR_CUDA;
+    }
 }
 
 size_t ctx_attn_window_workspace_size(int B, int S, int Hq, int Hkv, int D, int P, int causal, int window_left,

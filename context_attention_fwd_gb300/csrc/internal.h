@@ -144,13 +144,17 @@ struct BwdParams {
     int head_major;  // launch order of the attention kernel (grid_pos in walk.cuh)
     int debug;       // kDebug* bits (0 in normal use)
     int pdl;         // launch with programmatic stream serialization (launch_kernel)
-    // windowed calls (WinGrid in walk.cuh): the query tiles that see one of the
-    // first sink_tiles KV tiles are split over sink_parts CTAs of sink_per
-    // tiles each, which write fp32 partial dK (unscaled) / dV to dkv_part
-    // [sink_parts][B][Hkv][sink_rows][2][D] when there is more than one
+    // windowed calls (win_work in walk.cuh): the query heads of a group are
+    // split over hsplit CTAs as above, for every D, and the query tiles that
+    // see one of the first sink_tiles KV tiles over sink_parts CTAs of
+    // sink_per tiles each.  Where that makes more than one piece of a KV tile,
+    // each writes fp32 partial dK (unscaled) / dV and window_reduce_kernel sums
+    // them: sink tiles in sink_part [sink_parts * hsplit][B][Hkv][sink_rows][2][D]
+    // (piece part * hsplit + split), the others in dkv_part
     int windowed;
     Window win;
     int sink_tiles, sink_parts, sink_per, sink_rows;
+    float* sink_part;
 };
 
 int launch_attn_fwd(const FwdParams& p, int D, cudaStream_t s);

@@ -249,7 +249,7 @@ struct WinWork {
 __host__ __device__ __forceinline__ int win_grid(int ntiles, int sink_tiles, int sink_parts) {
     return sink_tiles * sink_parts + ntiles - sink_tiles;
 }
-__device__ __forceinline__ WinWork win_work(int i, int sink_tiles, int sink_parts) {
+__host__ __device__ __forceinline__ WinWork win_work(int i, int sink_tiles, int sink_parts) {
     const int n = sink_tiles * sink_parts;
     return i < n ? WinWork{i / sink_parts, i % sink_parts} : WinWork{sink_tiles + i - n, -1};
 }
@@ -260,6 +260,18 @@ __host__ __device__ __forceinline__ WinQ win_part_q(const ChunkTable& ct, const 
 }
 // A part outside the window's reach only touches sink rows.
 __host__ __device__ __forceinline__ bool win_overlap(const WinQ& a, const WinQ& b) { return a.t0 < b.t1 && b.t0 < a.t1; }
+
+// Where a windowed CTA's piece of a KV tile leaves its partial rows, or null
+// when it is the tile's only piece (BwdParams in internal.h).
+template <int D>
+__device__ __forceinline__ float* win_part_rows(const BwdParams& p, const WinWork& w, int split, int b, int hk,
+                                                int kv_start) {
+    const bool sink = w.part >= 0;
+    float* base = sink ? p.sink_part : p.dkv_part;
+    if (!base) return nullptr;
+    const size_t piece = sink ? w.part * p.hsplit + split : split;
+    return base + (((piece * p.B + b) * p.Hkv + hk) * (sink ? p.sink_rows : p.S) + kv_start) * 2 * D;
+}
 
 struct WinQWalk {
     const ChunkTable* ct;

@@ -51,13 +51,17 @@ def test_backward_refuses_before_launch(lib):
 
 def test_workspace_covers_every_chunking(lib):
     n = lambda S, P, left, sinks, D=128: ctx.window_workspace_size(1, S, 4, 2, D, P, (left, 0), sinks, True)
-    assert n(1000, 4, 100, 0) == lib.ctx_attn_workspace_size(1, 1000, 4, 2, 128, 4, 0)
-    # sinks add the partial rows of at most 64 parts over all sink tiles
+    # few KV tiles: room for a head split's partial rows (two query heads a group)
+    base = lib.ctx_attn_workspace_size(1, 1000, 4, 2, 128, 4, 0)
+    assert n(1000, 4, 100, 0) == base + 2 * 2 * 1000 * 2 * 128 * 4
+    # many: none
+    assert n(60000, 4, 100, 0) == lib.ctx_attn_workspace_size(1, 60000, 4, 2, 128, 4, 0)
+    # sinks add the partial rows of at most 64 parts (and head splits) over all sink tiles
     for S, P, left, sinks in ((32760, 8, 1023, 4), (65536, 64, 0, 1), (32760, 1, 100, 2000), (9000, 3, 10, 9000)):
         extra = n(S, P, left, sinks) - n(S, P, left, 0)
         rows = min(S, sinks + 128)
-        assert 0 <= extra <= 64 * 2 * rows * 2 * 128 * 4 + 256
-        assert extra <= (64 + 64) * 2 * 2 * 128 * 128 * 4 * 2
+        assert 0 <= extra <= 2 * 64 * 2 * rows * 2 * 128 * 4 + 256
+        assert extra <= 2 * (64 + 64) * 2 * 2 * 128 * 128 * 4 * 2
     assert lib.ctx_attn_window_workspace_size(1, 1000, 4, 2, 128, 4, 1, -2, 0, 0) == 0
     assert lib.ctx_attn_window_workspace_size(1, 1000, 4, 3, 128, 4, 1, 5, 0, 0) == 0
     assert lib.ctx_attn_window_workspace_size(1, 3, 4, 2, 128, 4, 1, 5, 0, 0) == 0
