@@ -216,14 +216,17 @@ def _packed(t, name, dtype, device):
     return _PACK(t.data_ptr(), *shape, *stride[:3])
 
 
-def _result(given, name, like, heads=None):
+def _result(given, name, like):
     """(tensor, descriptor) of a result: the one given, or a new one of
-    `like`'s type, storage order and shape (with `heads` heads)."""
+    `like`'s type, shape and storage order."""
     if given is not None:
         return given, _packed(given, name, like.dtype, like.device)
-    B, S, H, D = like.shape
-    H = heads or H
-    if like.stride(0) >= like.stride(1):  # [B,S,H,D] storage
+    shape, stride = like.shape, like.stride()
+    if like.is_contiguous():
+        t = torch.empty_like(like)
+        return t, _PACK(t.data_ptr(), *shape, *stride[:3])
+    B, S, H, D = shape
+    if stride[0] >= stride[1]:  # [B,S,H,D] storage
         t = torch.empty((B, S, H, D), dtype=like.dtype, device=like.device)
         return t, _PACK(t.data_ptr(), B, S, H, D, S * H * D, H * D, D)
     t = torch.empty((S, B, H, D), dtype=like.dtype, device=like.device).permute(1, 0, 2, 3)

@@ -19,7 +19,7 @@
 // heads; the sines and cosines of a token are computed once, by the warp
 // together, for all of its query and key heads.
 //   16-byte groups: eight pairs per thread, two 16-byte accesses (for 16-bit
-//     types) per tensor; needs D, R multiples of 16 and 16-byte aligned rows.
+//     types) per tensor; needs 16-byte aligned rows and D a multiple of 16.
 //   single pairs: any even D and R, any strides; one head per pass.
 #include <math.h>
 #include <string.h>
@@ -44,6 +44,8 @@ constexpr int kGradBlocks = 3;  // of them on an SM
 constexpr int kMaxGradBlocks = 1024;  // blocks of the backward that leave partial weight gradients
 
 enum { kRotate = 0, kNorm = 1, kNormGrad = 2 };
+// How a thread's sixteen elements of a row form pairs (16-byte groups below).
+enum { kHalf = 0, kInter = 1, kShifted = 2 };
 
 struct RopeRows {  // one logical [B,S,H,D] tensor
     const void* p;
@@ -123,22 +125,30 @@ __device__ __forceinline__ int angle_slot(int i, int ngroups) {
 template <bool kVec>
 __device__ __forceinline__ void token_angles(const RopeParams& p, const Unit& u, float2* cs) {
     __syncwarp();  // the previous token's are no longer read
-    for (int i = lane_id(); i < p.rot / 2; i += 32) {
-        int axis = 0;
-        for (int a = 0; a + 1 < p.n_axes; ++a) axis += i >= p.sec_end[a];
-        const int64_t at = p.pos ? p.pos[u.b * p.pos_sb + u.s * p.pos_ss + axis * p.pos_sa] : p.offset + u.s;
-        const int32_t turn = (int32_t)(((uint64_t)at * p.turns[i]) >> 32);
-        float si, co;
-        sincospif((float)turn * 4.656612873077393e-10f, &si, &co);  // 2^-31: half turns
-        cs[angle_slot<kVec>(i, p.D / 16)] = make_float2(co * p.m, si * p.sin_sign);
+    for (int i = lane_id(); i < p.D / 2; i += 32) {
+        float2 v = make_float2(1.f, 0.f);  // the part that is not rotated
+        if (i < p.rot / 2) {
+            int axis = 0;
+            for (int a = 0; a + 1 < p.n_axes; ++a) axis += i >= p.sec_end[a];
+            const int64_t at = p.pos ? p.pos[u.b * p.pos_sb + u.s * p.pos_ss + axis * p.pos_sa] : p.offset + u.s;
+            const int32_t turn = (int32_t)(((uint64_t)at * p.turns[i]) >> 32);
+            float si, co;
+            sincospif((float)turn * 4.656612873077393e-10f, &si, &co);  // 2^-31: half turns
+            v = make_float2(co * p.m, si * p.sin_sign);
+        }
+        cs[angle_slot<kVec>(i, p.D / 16)] = v;
     }
     __syncwarp();
 }
 
 // ------------------------------------------------------- 16-byte groups
 // A thread's 16 elements of a row, as stored: eight neighbouring twos.
-// Interleaved: two j is pair j.  Half: twos 0..3 are the first elements of
-// pairs 0..7, twos 4..7 their second ones.
+//   kInter    two j is pair j.
+//   kHalf     twos 0..3 are the first elements of pairs 0..7, twos 4..7 their
+//             second ones (R a multiple of 16).
+//   kShifted  the half layout for any other R: sixteen consecutive elements,
+//             whose partners, R / 2 away, other threads hold; they come through
+//             shared memory (Partners).
 template <typename T>
 struct Group {
     uint4 u[sizeof(T)];  // 16 elements
@@ -187,17 +197,58 @@ struct Group {
     }
 };
 
+// The warp's rows in shared memory, word w of every lane side by side: writing
+// a thread's own words and reading its partners' (all the same distance away)
+// are both free of bank conflicts.
+template <typename T>
+struct Partners {
+    static constexpr int kWords = 4 * sizeof(T);  // of a lane
+    uint32_t* buf;
+    __device__ __forceinline__ void put(const Group<T>& g) const {
+        __syncwarp();  // the previous row's are no longer read
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) buf[i * 32 + lane_id()] = g.word(i);
+        __syncwarp();
+    }
+    // element e (of the row of this thread's head)
+    __device__ __forceinline__ float at(int e, int row_lane0) const {
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(buf[(e & 15) * 32 + row_lane0 + (e >> 4)]);
+        } else {
+            const int w = e >> 1;
+            const T* two = reinterpret_cast<const T*>(buf + (w & 7) * 32 + row_lane0 + (w >> 3));
+            return to_f<T>(two[e & 1]);
+        }
+    }
+    // The partners of elements e, e + 1 (e even): R / 2 further, or back; an
+    // element past R is its own (its sine is zero).
+    __device__ __forceinline__ float2 pair(const RopeParams& p, int e, int row_lane0) const {
+        const int h = p.rot / 2;
+        const int e0 = e < h ? e + h : (e < p.rot ? e - h : e);
+        if (sizeof(T) == 2 && (h & 1) == 0) {
+            const int w = e0 >> 1;
+            Group<T> g;
+            g.word(0) = buf[(w & 7) * 32 + row_lane0 + (w >> 3)];
+            return g.two(0);
+        }
+        const int f = e + 1, e1 = f < h ? f + h : (f < p.rot ? f - h : f);
+        return make_float2(at(e0, row_lane0), at(e1, row_lane0));
+    }
+};
+
 struct RowThread {  // which part of which head's row a thread holds
     int group, slot;
+    int lane0;  // first lane of this head's row
     bool live;
     int2 at;  // where its two runs of eight elements start
-    __device__ __forceinline__ RowThread(const RopeParams& p, bool inter) {
+    __device__ __forceinline__ RowThread(const RopeParams& p, int style) {
         const int lane = lane_id();
         slot = lane >> p.log2_L;
         group = lane & (p.L - 1);
+        lane0 = lane - group;
         live = group < p.D / 16;
         if (!live) group = 0;  // reads the first group's elements; kept out of sums and stores
-        at = !inter && group * 8 < p.rot / 2 ? make_int2(group * 8, p.rot / 2 + group * 8)
+        at = style == kHalf && group * 8 < p.rot / 2 ? make_int2(group * 8, p.rot / 2 + group * 8)
                                              : make_int2(group * 16, group * 16 + 8);
     }
     __device__ __forceinline__ float row_sum(const RopeParams& p, float v) const {
@@ -207,11 +258,17 @@ struct RowThread {  // which part of which head's row a thread holds
             if (o < p.L) v += __shfl_xor_sync(0xffffffffu, v, o);
         return v;
     }
-    // (cosine, sine) of pairs 2j, 2j + 1; 1, 0 in the part that is not rotated
+    // (cosine, sine) of pairs 2j, 2j + 1
     __device__ __forceinline__ float4 angles(const RopeParams& p, const float2* cs, int j) const {
-        return group * 8 < p.rot / 2
-                   ? *reinterpret_cast<const float4*>(cs + angle_slot<true>(group * 8 + 2 * j, p.D / 16))
-                   : make_float4(1.f, 0.f, 1.f, 0.f);
+        return *reinterpret_cast<const float4*>(cs + angle_slot<true>(group * 8 + 2 * j, p.D / 16));
+    }
+    // kShifted: (cosine, sine) of the pair element e belongs to, the sine with
+    // the sign its partner enters with
+    __device__ __forceinline__ float2 angle_of(const RopeParams& p, const float2* cs, int e) const {
+        const int h = p.rot / 2;
+        if (e >= p.rot) return make_float2(1.f, 0.f);
+        const float2 v = cs[angle_slot<true>(e < h ? e : e - h, p.D / 16)];
+        return make_float2(v.x, e < h ? -v.y : v.y);
     }
     __device__ __forceinline__ void weights(const RopeParams& p, int side, float2* w) const {
         if (!p.w[side]) {
@@ -250,13 +307,15 @@ __device__ __forceinline__ float row_rsqrt(float v) {
 //   half         ya = a (wa c) + b (-wb s),  yb = b (wb c) + a (wa s)
 // in two-lane fp32 instructions.  kBatch passes are loaded before the first
 // is computed, so that a warp has kBatch kilobytes (16-bit types) in flight.
-template <typename T, bool kInter, bool kNormed, int kBatch, int kBlocks>
+template <typename T, int kStyle, bool kNormed, int kBatch, int kBlocks>
 __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float2 cs_all[kWarps][kMaxRopeDim / 2];
+    __shared__ uint32_t partners[kStyle == kShifted ? kWarps : 1][kStyle == kShifted ? 32 * Partners<T>::kWords : 1];
+    const Partners<T> pt{partners[kStyle == kShifted ? warp_id() : 0]};
     float2* cs = cs_all[warp_id()];
     const int64_t un = (int64_t)blockIdx.x * kWarps + warp_id();
     if (un >= (int64_t)p.B * p.S * p.units_per_token) return;
-    const RowThread th(p, kInter);
+    const RowThread th(p, kStyle);
     const int per_pass = 32 >> p.log2_L;
     const float inv_d = 1.f / (float)p.D;
     const Unit u = unit_at(p, un);
@@ -287,9 +346,9 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid
                 float2 w[8];
                 if constexpr (kNormed) th.weights(p, side, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; kStyle != kShifted && j < 4; ++j) {
                     const float4 a = th.angles(p, cs, j);  // pairs 2j, 2j + 1
-                    if constexpr (kInter) {
+                    if constexpr (kStyle == kInter) {
                         const float2 w0 = kNormed ? w[2 * j] : make_float2(1.f, 1.f);
                         const float2 w1 = kNormed ? w[2 * j + 1] : make_float2(1.f, 1.f);
                         k[2 * j] = make_float2(w0.x * a.x, w0.y * a.x);
@@ -303,6 +362,21 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid
                         k[4 + j] = make_float2(wb.x * a.x, wb.y * a.z);
                         k[8 + j] = make_float2(-wb.x * a.y, -wb.y * a.w);
                         k[12 + j] = make_float2(wa.x * a.y, wa.y * a.w);
+                    }
+                }
+                if constexpr (kStyle == kShifted) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int e = th.group * 16 + 2 * j, hf = p.rot / 2;
+                        const float2 a0 = th.angle_of(p, cs, e), a1 = th.angle_of(p, cs, e + 1);
+                        float2 wo = make_float2(1.f, 1.f), wp = wo;  // own weights, partners' weights
+                        if constexpr (kNormed) {
+                            wo = w[j];
+                            wp.x = weight_at(p, side, e < hf ? e + hf : (e < p.rot ? e - hf : e));
+                            wp.y = weight_at(p, side, e + 1 < hf ? e + 1 + hf : (e + 1 < p.rot ? e + 1 - hf : e + 1));
+                        }
+                        k[j] = make_float2(wo.x * a0.x, wo.y * a1.x);
+                        k[8 + j] = make_float2(wp.x * a0.y, wp.y * a1.y);
                     }
                 }
                 have_k = true;
@@ -320,10 +394,12 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid
                     r2 = make_float2(r, r);
                 }
                 Group<T> y;
-                if constexpr (kInter) {
+                if constexpr (kStyle == kShifted) pt.put(raw[i]);
+                if constexpr (kStyle != kHalf) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        float2 v = ffma2(raw[i].two(j), k[j], fmul2(raw[i].swapped(j), k[8 + j]));
+                        const float2 other = kStyle == kInter ? raw[i].swapped(j) : pt.pair(p, th.group * 16 + 2 * j, th.lane0);
+                        float2 v = ffma2(raw[i].two(j), k[j], fmul2(other, k[8 + j]));
                         if constexpr (kNormed) v = fmul2(v, r2);
                         y.set(j, v);
                     }
@@ -348,12 +424,14 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid
 // keys', so that the weight gradients of one side stay in its registers; each
 // block leaves its sums (over its warps, in a fixed order) for
 // weight_grad_kernel.
-template <typename T, bool kInter, int kBatch, int kBlocks>
+template <typename T, int kStyle, int kBatch, int kBlocks>
 __global__ void __launch_bounds__(32 * kGradWarps, kBlocks) norm_grad_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float2 cs_all[kGradWarps][kMaxRopeDim / 2];
     __shared__ float sums[kGradWarps][kMaxRopeDim];
+    __shared__ uint32_t partners[kStyle == kShifted ? kGradWarps : 1][kStyle == kShifted ? 32 * Partners<T>::kWords : 1];
+    const Partners<T> pt{partners[kStyle == kShifted ? warp_id() : 0]};
     float2* cs = cs_all[warp_id()];
-    const RowThread th(p, kInter);
+    const RowThread th(p, kStyle);
     const int per_pass = 32 >> p.log2_L;
     const int64_t units = (int64_t)p.B * p.S * p.units_per_token;
     const float inv_d = 1.f / (float)p.D;
@@ -374,7 +452,9 @@ __global__ void __launch_bounds__(32 * kGradWarps, kBlocks) norm_grad_kernel(con
             const T* xt = token_row<T>(p.x[side], u.b, u.s);
             const T* gt = token_row<T>(p.g[side], u.b, u.s);
             T* yt = token_row<T>(p.y[side], u.b, u.s);
-            float2 c[8];  // interleaved: cos, sin of pair j; half: cos of pairs 2j, 2j + 1, then their sines
+            // interleaved: cos, sin of pair j; half: cos of pairs 2j, 2j + 1, then
+            // their sines; shifted: cos of elements 2j, 2j + 1, then their signed sines
+            float2 c[kStyle == kShifted ? 16 : 8];
             bool have_angles = false;
 #pragma unroll 1
             for (int ps = p0; ps < p1; ps += kBatch) {
@@ -388,11 +468,21 @@ __global__ void __launch_bounds__(32 * kGradWarps, kBlocks) norm_grad_kernel(con
                     }
                 if (!have_angles) {
                     token_angles<true>(p, u, cs);
+                    if constexpr (kStyle == kShifted) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 a = th.angles(p, cs, j);
-                        c[kInter ? 2 * j : j] = kInter ? make_float2(a.x, a.y) : make_float2(a.x, a.z);
-                        c[kInter ? 2 * j + 1 : 4 + j] = kInter ? make_float2(a.z, a.w) : make_float2(a.y, a.w);
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 a0 = th.angle_of(p, cs, th.group * 16 + 2 * j);
+                            const float2 a1 = th.angle_of(p, cs, th.group * 16 + 2 * j + 1);
+                            c[j] = make_float2(a0.x, a1.x);
+                            c[8 + j] = make_float2(-a0.y, -a1.y);  // the transposed rotation
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 a = th.angles(p, cs, j);
+                            c[kStyle == kInter ? 2 * j : j] = kStyle == kInter ? make_float2(a.x, a.y) : make_float2(a.x, a.z);
+                            c[kStyle == kInter ? 2 * j + 1 : 4 + j] = kStyle == kInter ? make_float2(a.z, a.w) : make_float2(a.y, a.w);
+                        }
                     }
                     have_angles = true;
                 }
@@ -402,7 +492,12 @@ __global__ void __launch_bounds__(32 * kGradWarps, kBlocks) norm_grad_kernel(con
                     const int h = (ps + i) * per_pass + th.slot;
                     const bool on = h < H;
                     float2 g[8], q = make_float2(0.f, 0.f), gq = q;
-                    if constexpr (kInter) {
+                    if constexpr (kStyle == kShifted) {
+                        pt.put(grad[i]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            g[j] = ffma2(grad[i].two(j), c[j], fmul2(pt.pair(p, th.group * 16 + 2 * j, th.lane0), c[8 + j]));
+                    } else if constexpr (kStyle == kInter) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float2 v = grad[i].two(j);
@@ -512,7 +607,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) rope_pairs_kernel(const __gri
                     b[k] = on ? to_f<T>(x[e[k].y]) : 0.f;
                     sx = fmaf(a[k], a[k], fmaf(b[k], b[k], sx));
                     if constexpr (kMode == kNormGrad) {
-                        const float2 v = on && i < p.rot / 2 ? cs[i] : make_float2(1.f, 0.f);
+                        const float2 v = on ? cs[i] : make_float2(1.f, 0.f);
                         const float g1 = on ? to_f<T>(g[e[k].x]) : 0.f, g2 = on ? to_f<T>(g[e[k].y]) : 0.f;
                         ga[k] = g1 * v.x + g2 * v.y;
                         gb[k] = g2 * v.x - g1 * v.y;
@@ -541,7 +636,7 @@ __global__ void __launch_bounds__(32 * kGradWarps) rope_pairs_kernel(const __gri
                         ya = fmaf(ga[k] * wa[k], r, a[k] * kx);
                         yb = fmaf(gb[k] * wb[k], r, b[k] * kx);
                     } else {
-                        const float2 v = i < p.rot / 2 ? cs[i] : make_float2(1.f, 0.f);
+                        const float2 v = cs[i];
                         const float xa = a[k] * r * wa[k], xb = b[k] * r * wb[k];
                         ya = xa * v.x - xb * v.y;
                         yb = xb * v.x + xa * v.y;
@@ -592,15 +687,29 @@ __global__ void weight_grad_kernel(const float* __restrict__ part, int blocks, i
 template <typename T, int kMode>
 cudaError_t launch_rope_mode(const RopeParams& p, bool vec, unsigned grid, cudaStream_t s) {
     const dim3 blk(32 * kWarps), gblk(32 * kGradWarps);
+    const int style = p.interleaved ? kInter : p.rot % 16 == 0 ? kHalf : kShifted;
     if (!vec) return launch_kernel(false, rope_pairs_kernel<T, kMode>, dim3(grid), gblk, 0, s, p);
     if constexpr (kMode == kNormGrad) {
         constexpr int kBatch = sizeof(T) == 4 ? 1 : 2;
-        return p.interleaved ? launch_kernel(false, norm_grad_kernel<T, true, kBatch, kGradBlocks>, dim3(grid), gblk, 0, s, p)
-                             : launch_kernel(false, norm_grad_kernel<T, false, kBatch, kGradBlocks>, dim3(grid), gblk, 0, s, p);
+        auto kern = style == kInter ? norm_grad_kernel<T, kInter, kBatch, kGradBlocks>
+                    : style == kHalf ? norm_grad_kernel<T, kHalf, kBatch, kGradBlocks>
+                                     : norm_grad_kernel<T, kShifted, 1, kGradBlocks>;
+        return launch_kernel(false, kern, dim3(grid), gblk, 0, s, p);
     } else {
-        constexpr int kBatch = sizeof(T) == 4 ? 2 : kMode == kNorm ? 6 : 3, kBlocks = kMode == kNorm ? 2 : 3;
-        return p.interleaved ? launch_kernel(false, rope_kernel<T, true, kMode == kNorm, kBatch, kBlocks>, dim3(grid), blk, 0, s, p)
-                             : launch_kernel(false, rope_kernel<T, false, kMode == kNorm, kBatch, kBlocks>, dim3(grid), blk, 0, s, p);
+        // Passes in flight against warps on an SM.  The norm's six (the longest
+        // batch that does not spill at two blocks) took 138 us on 32760 tokens
+        // of 24/24 heads, D = 128, two at three blocks 143; rows of fewer passes
+        // have nothing to fill six with.
+        constexpr bool kNormed = kMode == kNorm;
+        constexpr int kLong = sizeof(T) == 4 ? 2 : kNormed ? 6 : 3, kLongBlocks = kNormed ? 2 : 3;
+        constexpr int kShort = 2, kShortBlocks = 3;
+        const bool few = kNormed && std::max(p.passes[0], p.passes[1]) <= 3;
+        auto kern = style == kInter ? (few ? rope_kernel<T, kInter, kNormed, kShort, kShortBlocks>
+                                           : rope_kernel<T, kInter, kNormed, kLong, kLongBlocks>)
+                    : style == kHalf ? (few ? rope_kernel<T, kHalf, kNormed, kShort, kShortBlocks>
+                                            : rope_kernel<T, kHalf, kNormed, kLong, kLongBlocks>)
+                                     : rope_kernel<T, kShifted, kNormed, kShort, 2>;
+        return launch_kernel(false, kern, dim3(grid), blk, 0, s, p);
     }
 }
 
@@ -694,7 +803,7 @@ int rope_call(const char* name, int mode, const ctx_tensor_t* const x[2], const 
         p.interleaved = 1;
     }
     p.sin_sign = inverse ? -p.m : p.m;
-    const bool vec = aligned && D % 16 == 0 && p.rot % 16 == 0;
+    const bool vec = aligned && D % 16 == 0;
     int groups = vec ? (int)D / 16 : 32;
     while ((1 << p.log2_L) < groups) ++p.log2_L;
     p.L = 1 << p.log2_L;

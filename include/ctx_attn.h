@@ -275,8 +275,8 @@ int ctx_seq_head_exchange(const ctx_tensor_t* x, void* y, int ring, int ulysses,
  * The steps that stand between a model's projections and its attention call.
  * They take logical [B,S,H,D] tensors as the attention does, but of any of
  * three element types, any even D up to 512 and any strides whose D stride is
- * 1 (rows on 16-byte boundaries with D and rot_dim multiples of 16 take the
- * wide-access kernels; anything else is right, and slower).  q and k may have
+ * 1 (rows on 16-byte boundaries with D a multiple of 16 take the wide-access
+ * kernels; anything else is right, and slower).  q and k may have
  * different head counts; k (with its result) may be NULL.  A result may be
  * its own input (same data and strides); it must not overlap it otherwise. */
 typedef enum { CTX_DTYPE_BF16 = 0, CTX_DTYPE_FP16 = 1, CTX_DTYPE_FP32 = 2 } ctx_dtype_t;

@@ -81,7 +81,14 @@ CASES = [  # B, S, Hq, Hk, D, rot, interleaved, dtype, layout, positions
     (1, 9, 7, 3, 512, 512, False, F32, "bshd", "each"),
     (1, 9, 2, 1, 512, 510, True, BF, "bshd", "shared"),
     (1, 9, 2, 1, 510, 254, False, BF, "bshd", "shared"),
+    (2, 19, 5, 2, 128, 50, False, BF, "bshd", "each"),      # half pairs whose halves are not whole groups:
+    (1, 37, 24, 4, 80, 40, False, FP, "sbhd", "shared"),    # partners through shared memory, in twos
+    (1, 11, 3, 2, 64, 22, False, F32, "bshd", "each"),      # or one by one
+    (1, 7, 9, 1, 512, 6, False, BF, "bshd", "offset"),
+    (1, 7, 2, 2, 16, 10, False, F32, "bshd", "offset"),
+    (1, 40, 3, 2, 48, 48, False, BF, "bshd", "each"),       # three groups of a row's four lanes
     (2, 3000, 4, 2, 64, 16, True, BF, "bshd", "shared"),    # many tokens: one unit per token
+    (1, 5000, 16, 2, 64, 28, False, BF, "bshd", "shared"),
     (16, 1, 24, 4, 256, 256, True, FP, "bshd", "each"),     # newest tokens
 ]
 
@@ -170,8 +177,8 @@ def test_several_position_axes(batched, D):
         ctx.rope_fwd(q, k, table, positions=p[..., :2].cuda())
 
 
-@pytest.mark.parametrize("shift", [0, 1])  # 16-byte rows; rows off the boundary (single-pair kernel)
-def test_views_of_one_projection_in_place(shift):
+@pytest.mark.parametrize("shift,rot", [(0, 32), (0, 20), (1, 32)])  # 16-byte rows (twice); off the boundary (single pairs)
+def test_views_of_one_projection_in_place(shift, rot):
     """q and k as views of a packed [B,S,(Hq+2Hk) D] projection, rotated in
     place: v, the padding and everything around the views stay as they were."""
     g = torch.Generator().manual_seed(4)
@@ -184,12 +191,12 @@ def test_views_of_one_projection_in_place(shift):
     k = rows[:, :, Hq * D:(Hq + Hk) * D].unflatten(2, (Hk, D))
     q0, k0 = q.double().cpu(), k.double().cpu()
     w = (1 + 0.3 * torch.randn(D, generator=g)).cuda()
-    table = ctx.rope_table(32)
+    table = ctx.rope_table(rot)
     ctx.qk_norm_rope_fwd(q, k, w, w, table, offset=5, q_out=q, k_out=k)
     ang = ref.angles(table.turns, (5 + torch.arange(S)).expand(B, S))
     for x, x0 in ((q, q0), (k, k0)):
         n = ref.norm(x0, w.double().cpu(), 1e-6)
-        close("view", x, ref.rotate(n, ang, 32, False), 2.0 ** -18 * _pair_len(n, 32, False), BF)
+        close("view", x, ref.rotate(n, ang, rot, False), 2.0 ** -18 * _pair_len(n, rot, False), BF)
     mask = torch.zeros_like(buf, dtype=torch.bool)
     mask[shift:shift + B * S * width].view(B, S, width)[:, :, :(Hq + Hk) * D] = True
     assert torch.equal(buf[~mask].view(torch.int16), before[~mask].view(torch.int16))
