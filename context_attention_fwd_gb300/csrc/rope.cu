@@ -40,7 +40,8 @@ namespace {
 constexpr int kMaxRopeDim = 512;
 constexpr int kWarps = 8;      // warps of a forward block
 constexpr int kGradWarps = 4;  // warps of a norm-gradient block
-constexpr int kGradBlocks = 3;  // of them on an SM
+constexpr int kGradBlocks = 4;  // of them on an SM
+constexpr int kGradBlocksShifted = 3;
 constexpr int kMaxGradBlocks = 1024;  // blocks of the backward that leave partial weight gradients
 
 enum { kRotate = 0, kNorm = 1, kNormGrad = 2 };
@@ -251,12 +252,18 @@ struct RowThread {  // which part of which head's row a thread holds
         at = style == kHalf && group * 8 < p.rot / 2 ? make_int2(group * 8, p.rot / 2 + group * 8)
                                              : make_int2(group * 16, group * 16 + 8);
     }
-    __device__ __forceinline__ float row_sum(const RopeParams& p, float v) const {
-        if (!live) v = 0.f;
+    // Sums over the row's lanes of N values at once (their shuffles overlap).
+    template <int N>
+    __device__ __forceinline__ void row_sums(const RopeParams& p, float (&v)[N]) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (!live) v[i] = 0.f;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1)
-            if (o < p.L) v += __shfl_xor_sync(0xffffffffu, v, o);
-        return v;
+            if (o < p.L) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+            }
     }
     // (cosine, sine) of pairs 2j, 2j + 1
     __device__ __forceinline__ float4 angles(const RopeParams& p, const float2* cs, int j) const {
@@ -390,7 +397,9 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid
                     float2 q = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) q = ffma2(raw[i].two(j), raw[i].two(j), q);
-                    const float r = row_rsqrt<T>(fmaf(th.row_sum(p, q.x + q.y), inv_d, p.eps));
+                    float sum[1] = {q.x + q.y};
+                    th.row_sums(p, sum);
+                    const float r = row_rsqrt<T>(fmaf(sum[0], inv_d, p.eps));
                     r2 = make_float2(r, r);
                 }
                 Group<T> y;
@@ -491,7 +500,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, kBlocks) norm_grad_kernel(con
                     if (ps + i >= p1) continue;
                     const int h = (ps + i) * per_pass + th.slot;
                     const bool on = h < H;
-                    float2 g[8], q = make_float2(0.f, 0.f), gq = q;
+                    float2 g[8];
                     if constexpr (kStyle == kShifted) {
                         pt.put(grad[i]);
 #pragma unroll
@@ -511,15 +520,21 @@ __global__ void __launch_bounds__(32 * kGradWarps, kBlocks) norm_grad_kernel(con
                             g[4 + j] = fsub2(fmul2(g2, c[j]), fmul2(g1, c[4 + j]));
                         }
                     }
+                    float2 q0 = make_float2(0.f, 0.f), q1 = q0, gq0 = q0, gq1 = q0;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 x = raw[i].two(j);
-                        q = ffma2(x, x, q);
-                        gq = ffma2(fmul2(g[j], x), w[j], gq);
+                    for (int j = 0; j < 8; j += 2) {
+                        const float2 x0 = raw[i].two(j), x1 = raw[i].two(j + 1);
+                        q0 = ffma2(x0, x0, q0);
+                        q1 = ffma2(x1, x1, q1);
+                        gq0 = ffma2(fmul2(g[j], x0), w[j], gq0);
+                        gq1 = ffma2(fmul2(g[j + 1], x1), w[j + 1], gq1);
                     }
-                    const float sx = th.row_sum(p, q.x + q.y), sgx = th.row_sum(p, gq.x + gq.y);
-                    const float r = on ? row_rsqrt<T>(fmaf(sx, inv_d, p.eps)) : 0.f;
-                    const float kx = -r * r * r * (sgx * inv_d);
+                    q0 = fadd2(q0, q1);
+                    gq0 = fadd2(gq0, gq1);
+                    float sums2[2] = {q0.x + q0.y, gq0.x + gq0.y};  // x^2, g w x
+                    th.row_sums(p, sums2);
+                    const float r = on ? row_rsqrt<T>(fmaf(sums2[0], inv_d, p.eps)) : 0.f;
+                    const float kx = -r * r * r * (sums2[1] * inv_d);
                     const float2 r2 = make_float2(r, r), k2 = make_float2(kx, kx);
                     Group<T> y;
 #pragma unroll
@@ -690,10 +705,12 @@ cudaError_t launch_rope_mode(const RopeParams& p, bool vec, unsigned grid, cudaS
     const int style = p.interleaved ? kInter : p.rot % 16 == 0 ? kHalf : kShifted;
     if (!vec) return launch_kernel(false, rope_pairs_kernel<T, kMode>, dim3(grid), gblk, 0, s, p);
     if constexpr (kMode == kNormGrad) {
-        constexpr int kBatch = sizeof(T) == 4 ? 1 : 2;
+        // one pass and four blocks (254 us on 32760 tokens of 24/24 heads, D = 128;
+        // two passes and three blocks 260): warps hide the loads, registers do not
+        constexpr int kBatch = 1;
         auto kern = style == kInter ? norm_grad_kernel<T, kInter, kBatch, kGradBlocks>
                     : style == kHalf ? norm_grad_kernel<T, kHalf, kBatch, kGradBlocks>
-                                     : norm_grad_kernel<T, kShifted, 1, kGradBlocks>;
+                                     : norm_grad_kernel<T, kShifted, 1, kGradBlocksShifted>;
         return launch_kernel(false, kern, dim3(grid), gblk, 0, s, p);
     } else {
         // Passes in flight against warps on an SM.  The norm's six (the longest
@@ -822,7 +839,9 @@ int rope_call(const char* name, int mode, const ctx_tensor_t* const x[2], const 
     const bool walk = mode == kNormGrad || !vec;  // kernels whose warps walk many units
     const int warps = walk ? kGradWarps : kWarps;
     int64_t grid = (units + warps - 1) / warps;
-    if (walk) grid = std::min<int64_t>(grid, std::min<int64_t>((mode == kNormGrad ? kGradBlocks : 16LL) * sms, kMaxGradBlocks));
+    const bool shifted = !p.interleaved && p.rot % 16 != 0;
+    const int64_t per_sm = !vec ? 16 : shifted ? kGradBlocksShifted : kGradBlocks;
+    if (walk) grid = std::min<int64_t>(grid, std::min<int64_t>(per_sm * sms, kMaxGradBlocks));
     if (grid > INT32_MAX) return CTX_ERR_INVALID_ARG;
     const bool want_dw = mode == kNormGrad && (p.dw[0] || p.dw[1]);
     if (want_dw) {
