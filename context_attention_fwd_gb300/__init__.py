@@ -247,6 +247,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _scratch(nbytes, device, given):
+    """(pointer, bytes, tensor) of a call's workspace: the one given, or a new one."""
+    if given is None:
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+        return _ptr(t), nbytes, t
+    if given.device != device or not given.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {device}, got one on {given.device}")
+    return given.data_ptr(), given.numel() * given.element_size(), given
+
+
 def _stream(t: torch.Tensor):
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
@@ -390,10 +400,10 @@ def attn_window_bwd(q, k, v, out, lse, dout, P, window, sinks=0, chunk_offsets=N
     (dq, pq), (dk, pk), (dv, pv) = _result(dq, "dq", q), _result(dk, "dk", k), _result(dv, "dv", k)
     with _on(dev):
         nbytes = lib.ctx_attn_window_workspace_size(B, S, Hq, k.shape[2], D, P, int(causal), left, right, sinks)
-        ws, wsb = _workspace(nbytes, dev, workspace)
+        ws, wsb, _keep = _scratch(nbytes, dev, workspace)
         rc = lib.ctx_attn_window_bwd(*ins[:4], lse.data_ptr(), ins[4], P, _offsets(P, chunk_offsets), LAYOUT_BSHD,
                                      int(causal), left, right, sinks, float(scale) if scale else 0.0, pq, pk, pv,
-                                     _ptr(ws), wsb, _raw_stream(dev))
+                                     ws, wsb, _raw_stream(dev))
     _check(rc, "ctx_attn_window_bwd")
     return dq, dk, dv
 
@@ -425,10 +435,10 @@ def attn_decode(q, k, v, lengths=None, window=-1, sinks=0, scale=None, out=None,
     lse = _lse(lse, B, Hq, T, dev)
     left = min(window, (1 << 31) - 1)
     with _on(dev):
-        ws, wsb = _workspace(lib.ctx_attn_decode_workspace_size(B, T, Hq, k.shape[2], D, k.shape[1], left, sinks),
-                             dev, workspace)
+        ws, wsb, _keep = _scratch(
+            lib.ctx_attn_decode_workspace_size(B, T, Hq, k.shape[2], D, k.shape[1], left, sinks), dev, workspace)
         rc = lib.ctx_attn_decode(dq, dk, dv, _ptr(lengths), LAYOUT_BSHD, left, sinks, float(scale) if scale else 0.0,
-                                 do, lse.data_ptr(), _ptr(ws), wsb, _raw_stream(dev))
+                                 do, lse.data_ptr(), ws, wsb, _raw_stream(dev))
     _check(rc, "ctx_attn_decode")
     return out, lse
 
@@ -492,6 +502,12 @@ class RopeTable:
     interleaved: bool
     sections: tuple      # pairs per position axis
     magnitude: float
+
+    def __post_init__(self):
+        if (self.rot_dim < 2 or self.rot_dim % 2 or self.turns.dtype != torch.int64
+                or tuple(self.turns.shape) != (self.rot_dim // 2,) or not self.turns.is_contiguous()
+                or not 1 <= len(self.sections) <= 4 or sum(self.sections) != self.rot_dim // 2):
+            raise ValueError("turns: one contiguous int64 per pair; sections: up to four counts of pairs that sum to them")
 
     @functools.cached_property
     def _head(self):
@@ -575,7 +591,7 @@ def _rope_desc(table, positions, offset, B, S, device):
     if positions is None:
         if axes > 1:
             raise ValueError("a table with several position axes needs positions")
-        return _PACK_ROPE(*table._head, 0, 0, 0, 0, offset)
+        return _PACK_ROPE(*table._head, 0, 0, 0, 0, int(offset))
     if positions.dtype != torch.int64 or positions.device != device:
         raise ValueError(f"positions: expected int64 on {device}, got {positions.dtype} on {positions.device}")
     shape, stride = positions.shape, positions.stride()
@@ -590,7 +606,7 @@ def _rope_desc(table, positions, offset, B, S, device):
         sb, ss = (0 if shape[0] == 1 else stride[0]), stride[1]
     else:
         raise ValueError(f"positions: {tuple(positions.shape)} does not fit {B} sequences of {S} tokens")
-    return _PACK_ROPE(*table._head, positions.data_ptr(), sb, ss, sa, offset)
+    return _PACK_ROPE(*table._head, positions.data_ptr(), sb, ss, sa, 0)
 
 
 def _row_type(t, name):
@@ -696,10 +712,10 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, table, positions=None, offset
     dwq = torch.empty(D, dtype=torch.float32, device=dev) if dwq is None and wq is not None else dwq
     dwk = torch.empty(D, dtype=torch.float32, device=dev) if dwk is None and wk is not None else dwk
     need = lib.ctx_qk_norm_rope_workspace_size(D) if dwq is not None or dwk is not None else 0
-    ws, wsb = _workspace(need, dev, workspace)
+    ws, wsb, _keep = _scratch(need, dev, workspace)
     with _on(dev):
         rc = lib.ctx_qk_norm_rope_bwd(pg, ph, pq, pk, _ptr(wq), _ptr(wk), wt, eps, rope, dt, LAYOUT_BSHD, oq, ok,
-                                      _ptr(dwq), _ptr(dwk), _ptr(ws), wsb, _raw_stream(dev))
+                                      _ptr(dwq), _ptr(dwk), ws, wsb, _raw_stream(dev))
     _check(rc, "ctx_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 

@@ -212,3 +212,23 @@ def test_refusals():
     with pytest.raises(ctx.CtxError) as e:
         ctx.attn_decode(*inputs(1, 1, 3000, 8, 2, 128), workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.code == 3
+    with pytest.raises(ValueError):
+        ctx.attn_decode(*inputs(1, 1, 3000, 8, 2, 128), workspace=torch.empty(1 << 24, dtype=torch.uint8))
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, each with its own outputs and workspace."""
+    a = inputs(1, 1, 20000, 8, 2, 128, seed=1)
+    b = inputs(2, 1, 9000, 12, 4, 64, seed=2)
+    want = [ctx.attn_decode(*x, window=w, sinks=4) for x, w in ((a, -1), (b, 5000))]
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            got.append((0, ctx.attn_decode(*a, window=-1, sinks=4)))
+        with torch.cuda.stream(s2):
+            got.append((1, ctx.attn_decode(*b, window=5000, sinks=4)))
+    torch.cuda.synchronize()
+    for i, (out, lse) in got:
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])

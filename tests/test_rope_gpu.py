@@ -316,6 +316,12 @@ def test_refusals_on_the_gpu():
         ctx.rope_fwd(q, None, ctx.rope_table(64, device="cpu"))
     with pytest.raises(ValueError):
         ctx.qk_norm_rope_fwd(q, None, torch.ones(32, device="cuda"), None, table)
+    w = torch.ones(64, device="cuda")
+    for ws in (torch.empty(1 << 22, dtype=torch.uint8), torch.empty(1 << 23, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            ctx.qk_norm_rope_bwd(q, None, q, None, w, None, table, workspace=ws)
+    with pytest.raises(ctx.CtxError):
+        ctx.qk_norm_rope_bwd(q, None, q, None, w, None, table, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ctx.CtxError):
         ctx.rope_fwd(q, None, ctx.rope_table(128))
     with pytest.raises(ctx.CtxError):

@@ -170,3 +170,20 @@ def test_binding_refuses_host_tensors_and_types():
         ctx.rope_fwd(x, None, None)
     with pytest.raises(ValueError, match="go together"):
         ctx.qk_norm_rope_bwd(x, x, x, None, None, None, t)
+
+
+def test_table_is_checked_when_made_by_hand():
+    good = ctx.rope_table(8, device="cpu")
+    for kw in (dict(rot_dim=10), dict(turns=good.turns[:3]), dict(turns=good.turns.int()), dict(sections=(2, 1)),
+               dict(turns=torch.zeros(8, dtype=torch.int64)[::2])):
+        with pytest.raises(ValueError):
+            ctx.RopeTable(**{**dict(turns=good.turns, rot_dim=8, interleaved=False, sections=(4,), magnitude=1.0), **kw})
+
+
+def test_packed_descriptors_have_the_c_layout():
+    """The packed bytes are the ctypes structures of the same fields."""
+    t = ctx.rope_table(8, sections=(1, 2, 1), interleaved=True, magnitude=1.5, device="cpu")
+    r = ctx._Rope(t.turns.data_ptr(), 8, 1, 3, (ctypes.c_int * 4)(1, 2, 1, 0), 1.5, 48, 3, 2, 1, -5)
+    assert ctx._PACK_ROPE(*t._head, 48, 3, 2, 1, -5) == bytes(r)
+    d = ctx._Tensor(64, 1, 2, 3, 4, 5, 6, 7)
+    assert ctx._PACK(64, 1, 2, 3, 4, 5, 6, 7) == bytes(d)

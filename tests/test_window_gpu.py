@@ -261,3 +261,8 @@ def test_refusals():
         ctx.attn_window_fwd(q.float(), k, v, 1, 5)
     with pytest.raises(ctx.CtxError):
         ctx.attn_window_fwd(q, k, v, 65, 5)
+    out, lse = ctx.attn_window_fwd(q, k, v, 1, 5)
+    with pytest.raises(ValueError):
+        ctx.attn_window_bwd(q, k, v, out, lse, q, 1, 5, workspace=torch.empty(1 << 24, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        ctx.attn_window_bwd(q, k, v, out, lse[:, :, :-1], q, 1, 5)
