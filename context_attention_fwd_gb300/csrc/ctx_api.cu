@@ -567,8 +567,7 @@ int make_window(const WindowArgs& a, int S, int causal, Window* w) {
     return CTX_OK;
 }
 
-// Tiles that the window of one tile's rows reaches (an upper bound up to the
-// chunks' partial tiles).
+// Tiles that the window of one tile's rows reaches, at most.
 int window_tiles(const Window& w, int ntiles) {
     const int64_t n = ((int64_t)w.left + w.right + 2 * kTile - 2) / kTile + 1;
     return n < ntiles ? (int)n : ntiles;
@@ -689,15 +688,14 @@ void plan_window_bwd(BwdParams* p, int D) {
 size_t win_part_bytes(int B, int S, int Hq, int Hkv, int D, int hs) {
     return hs > 1 ? align256((size_t)hs * B * Hkv * S * 2 * D * 4) : 0;
 }
-size_t win_bwd_ws_bytes(int B, int S, int Hq, int Hkv, int D, int P, const Window& w) {
-    const size_t slots = (size_t)B * Hq * ntiles_upper(S, P) * kTile;
+size_t win_bwd_ws_bytes(int B, int S, int Hq, int Hkv, int D, const Window& w) {
+    const int nt = (S + kTile - 1) / kTile;
+    const size_t slots = (size_t)B * Hq * nt * kTile;
     const int hs = win_hsplit_cap(S, B, Hq, Hkv, D);
     size_t part = win_part_bytes(B, S, Hq, Hkv, D, hs);
     if (w.sinks > 0) {
-        // enough for any chunking: the sink rows end with a tile that starts
-        // before the last sink does
-        const int pieces = sink_parts_cap(w, (int)ntiles_upper(S, P)) * hs;
-        const size_t rows = std::min((size_t)S, (size_t)w.sinks + kTile);
+        const int pieces = sink_parts_cap(w, nt) * hs;
+        const size_t rows = std::min(S, (w.sinks + kTile - 1) / kTile * kTile);  // whole tiles
         if (pieces > 1) part += align256((size_t)pieces * B * Hkv * rows * 2 * D * 4);
     }
     return align256(slots * 4) * 2 + align256(slots * D * 4) + part;
@@ -739,6 +737,9 @@ int attn_fwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k
     if (win && (rc = make_window(*win, (int)S, causal, &p.win))) return rc;
     p.windowed = win ? 1 : 0;
     if ((rc = build_chunks((int)S, P, chunk_offsets, &p.ct))) return rc;
+    // a windowed walk meets the tiles around it whatever the chunks: their
+    // boundaries would only add partial tiles
+    if (win) build_chunks((int)S, 1, nullptr, &p.ct);
     const bool partials = flags & CTX_FLAG_MATERIALIZE_PARTIALS;
     if (partials) {
         const size_t need = fwd_ws_bytes((int)B, (int)S, (int)Hq, (int)D, P, flags);
@@ -826,11 +827,12 @@ int attn_bwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k
     BwdParams p;
     memset(&p, 0, sizeof(p));
     if ((rc = build_chunks((int)S, P, chunk_offsets, &p.ct))) return rc;
+    if (win) build_chunks((int)S, 1, nullptr, &p.ct);  // as in attn_fwd_call
     if (win) {
         if ((rc = make_window(*win, (int)S, causal, &p.win))) return rc;
         p.windowed = 1;
     }
-    const size_t need = win ? win_bwd_ws_bytes((int)B, (int)S, (int)Hq, (int)Hkv, (int)D, P, p.win)
+    const size_t need = win ? win_bwd_ws_bytes((int)B, (int)S, (int)Hq, (int)Hkv, (int)D, p.win)
                             : bwd_ws_bytes((int)B, (int)S, (int)Hq, (int)Hkv, (int)D, P);
     if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255))
         return CTX_ERR_WORKSPACE;
@@ -1026,7 +1028,7 @@ size_t ctx_attn_window_workspace_size(int B, int S, int Hq, int Hkv, int D, int 
     Window w;
     if (!sizes_ok(B, S, Hq, Hkv, D) || P < 1 || P > S || P > kMaxChunks) return 0;
     if (make_window(WindowArgs{window_left, window_right, sinks}, S, causal, &w)) return 0;
-    return win_bwd_ws_bytes(B, S, Hq, Hkv, D, P, w);
+    return win_bwd_ws_bytes(B, S, Hq, Hkv, D, w);
 }
 
 }  // extern "C"

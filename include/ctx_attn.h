@@ -182,7 +182,9 @@ int ctx_attn_bwd_noalloc(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx
  *
  * Everything else is as in ctx_attn_fwd / ctx_attn_bwd (layouts, chunks, GQA,
  * head dimensions 64, 128 and 256, scale, ownership, dk and dv with equal
- * strides); the result does not depend on P.  Like there, a 128-row tile of
+ * strides), but the chunks, which are checked, shape nothing here: the tiles
+ * are those of the whole sequence, and the result is the same for every P.
+ * Like there, a 128-row tile of
  * keys is multiplied whole, with probability 0 where masked: a non-finite
  * value in k or v reaches every query whose tile meets its tile, also one
  * that does not see that key. */

@@ -49,13 +49,16 @@ def test_backward_refuses_before_launch(lib):
     assert call(dk=strided) == 2  # dk and dv stored differently
 
 
-def test_workspace_covers_every_chunking(lib):
+def test_workspace_size(lib):
     n = lambda S, P, left, sinks, D=128: ctx.window_workspace_size(1, S, 4, 2, D, P, (left, 0), sinks, True)
     # few KV tiles: room for a head split's partial rows (two query heads a group)
-    base = lib.ctx_attn_workspace_size(1, 1000, 4, 2, 128, 4, 0)
-    assert n(1000, 4, 100, 0) == base + 2 * 2 * 1000 * 2 * 128 * 4
+    def base(S):  # row statistics and the fp32 dq accumulator of whole tiles
+        slots = 4 * -(-S // 128) * 128
+        return 2 * slots * 4 + slots * 128 * 4
+
+    assert n(1000, 4, 100, 0) == n(1000, 9, 100, 0) == base(1000) + 2 * 2 * 1000 * 2 * 128 * 4
     # many: none
-    assert n(60000, 4, 100, 0) == lib.ctx_attn_workspace_size(1, 60000, 4, 2, 128, 4, 0)
+    assert n(60000, 4, 100, 0) == base(60000)
     # sinks add the partial rows of at most 64 parts (and head splits) over all sink tiles
     for S, P, left, sinks in ((32760, 8, 1023, 4), (65536, 64, 0, 1), (32760, 1, 100, 2000), (9000, 3, 10, 9000)):
         extra = n(S, P, left, sinks) - n(S, P, left, 0)
