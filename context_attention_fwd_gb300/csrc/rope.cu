@@ -38,10 +38,12 @@ namespace ctxattn {
 namespace {
 
 constexpr int kMaxRopeDim = 512;
-constexpr int kWarps = 8;      // warps of a forward block
+constexpr int kWarps = 2;      // warps of a forward block
 constexpr int kGradWarps = 4;  // warps of a norm-gradient block
-constexpr int kGradBlocks = 4;  // of them on an SM
-constexpr int kGradBlocksShifted = 3;
+// Of them on an SM: 16-bit types at 128 registers; fp32 and the shifted pairs,
+// which hold twice the words or angles, at 168 (fp32 at 128 spills: 183 us
+// instead of 125 on 10000 tokens of 24/24 heads, D = 128).
+constexpr int kGradBlocks = 4, kGradBlocksWide = 3;
 constexpr int kMaxGradBlocks = 1024;  // blocks of the backward that leave partial weight gradients
 
 enum { kRotate = 0, kNorm = 1, kNormGrad = 2 };
@@ -328,7 +330,9 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid
     const Unit u = unit_at(p, un);
     const int first = u.part * p.per_unit, last = min(first + p.per_unit, p.passes[0] + p.passes[1]);
     bool have_angles = false;
-#pragma unroll 1
+    // both sides in line where registers allow: their strides and pointers are
+    // then constants of the launch, not indexed loads (133 -> 127 us, below)
+#pragma unroll(kNormed && kBatch > 2 ? 2 : 1)
     for (int side = 0; side < 2; ++side) {
         const int base = side ? p.passes[0] : 0;
         const int p0 = max(first - base, 0), p1 = min(last - base, p.passes[side]);
@@ -432,120 +436,144 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid
 // every warp walks many tokens, all of the queries' first and then all of the
 // keys', so that the weight gradients of one side stay in its registers; each
 // block leaves its sums (over its warps, in a fixed order) for
-// weight_grad_kernel.
-template <typename T, int kStyle, int kBatch, int kBlocks>
+// weight_grad_kernel.  A warp loads one pass ahead of the one it computes, over
+// the end of a token too; the weights wait in shared memory to make room.
+template <typename T, int kStyle, int kBlocks>
 __global__ void __launch_bounds__(32 * kGradWarps, kBlocks) norm_grad_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float2 cs_all[kGradWarps][kMaxRopeDim / 2];
     __shared__ float sums[kGradWarps][kMaxRopeDim];
+    __shared__ float4 ws[4][32];  // twos 2q, 2q + 1 of group g at [q][g]
     __shared__ uint32_t partners[kStyle == kShifted ? kGradWarps : 1][kStyle == kShifted ? 32 * Partners<T>::kWords : 1];
     const Partners<T> pt{partners[kStyle == kShifted ? warp_id() : 0]};
     float2* cs = cs_all[warp_id()];
     const RowThread th(p, kStyle);
     const int per_pass = 32 >> p.log2_L;
     const int64_t units = (int64_t)p.B * p.S * p.units_per_token;
+    const int64_t step = (int64_t)gridDim.x * kGradWarps, first = (int64_t)blockIdx.x * kGradWarps + warp_id();
     const float inv_d = 1.f / (float)p.D;
-#pragma unroll 1
+#pragma unroll
     for (int side = 0; side < 2; ++side) {
         if (p.passes[side] == 0) continue;
         const int H = p.H[side];
-        float2 w[8], dw[8];
-        th.weights(p, side, w);
+        __syncthreads();  // the other side's weights have been read
+        if (warp_id() == 0 && th.slot == 0) {
+            float2 w[8];
+            th.weights(p, side, w);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ws[q][lane_id()] = make_float4(w[2 * q].x, w[2 * q].y, w[2 * q + 1].x, w[2 * q + 1].y);
+        }
+        __syncthreads();
+        float2 dw[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[j] = make_float2(0.f, 0.f);
-        for (int64_t un = (int64_t)blockIdx.x * kGradWarps + warp_id(); un < units; un += (int64_t)gridDim.x * kGradWarps) {
-            const Unit u = unit_at(p, un);
-            // this unit's share of the side's passes
-            const int p0 = (int)((int64_t)p.passes[side] * u.part / p.units_per_token);
-            const int p1 = (int)((int64_t)p.passes[side] * (u.part + 1) / p.units_per_token);
-            if (p0 >= p1) continue;
-            const T* xt = token_row<T>(p.x[side], u.b, u.s);
-            const T* gt = token_row<T>(p.g[side], u.b, u.s);
-            T* yt = token_row<T>(p.y[side], u.b, u.s);
-            // interleaved: cos, sin of pair j; half: cos of pairs 2j, 2j + 1, then
-            // their sines; shifted: cos of elements 2j, 2j + 1, then their signed sines
-            float2 c[kStyle == kShifted ? 16 : 8];
-            bool have_angles = false;
-#pragma unroll 1
-            for (int ps = p0; ps < p1; ps += kBatch) {
-                Group<T> raw[kBatch], grad[kBatch];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i)
-                    if (ps + i < p1) {
-                        const int h = min((ps + i) * per_pass + th.slot, H - 1);
-                        raw[i].load(xt + h * p.x[side].sh, th.at);
-                        grad[i].load(gt + h * p.g[side].sh, th.at);
-                    }
-                if (!have_angles) {
-                    token_angles<true>(p, u, cs);
-                    if constexpr (kStyle == kShifted) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float2 a0 = th.angle_of(p, cs, th.group * 16 + 2 * j);
-                            const float2 a1 = th.angle_of(p, cs, th.group * 16 + 2 * j + 1);
-                            c[j] = make_float2(a0.x, a1.x);
-                            c[8 + j] = make_float2(-a0.y, -a1.y);  // the transposed rotation
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 a = th.angles(p, cs, j);
-                            c[kStyle == kInter ? 2 * j : j] = kStyle == kInter ? make_float2(a.x, a.y) : make_float2(a.x, a.z);
-                            c[kStyle == kInter ? 2 * j + 1 : 4 + j] = kStyle == kInter ? make_float2(a.z, a.w) : make_float2(a.y, a.w);
-                        }
-                    }
-                    have_angles = true;
-                }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    if (ps + i >= p1) continue;
-                    const int h = (ps + i) * per_pass + th.slot;
-                    const bool on = h < H;
-                    float2 g[8];
-                    if constexpr (kStyle == kShifted) {
-                        pt.put(grad[i]);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            g[j] = ffma2(grad[i].two(j), c[j], fmul2(pt.pair(p, th.group * 16 + 2 * j, th.lane0), c[8 + j]));
-                    } else if constexpr (kStyle == kInter) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float2 v = grad[i].two(j);
-                            g[j] = make_float2(fmaf(v.x, c[j].x, v.y * c[j].y), fmaf(v.y, c[j].x, -(v.x * c[j].y)));
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 g1 = grad[i].two(j), g2 = grad[i].two(4 + j);
-                            g[j] = ffma2(g1, c[j], fmul2(g2, c[4 + j]));
-                            g[4 + j] = fsub2(fmul2(g2, c[j]), fmul2(g1, c[4 + j]));
-                        }
-                    }
-                    float2 q0 = make_float2(0.f, 0.f), q1 = q0, gq0 = q0, gq1 = q0;
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        const float2 x0 = raw[i].two(j), x1 = raw[i].two(j + 1);
-                        q0 = ffma2(x0, x0, q0);
-                        q1 = ffma2(x1, x1, q1);
-                        gq0 = ffma2(fmul2(g[j], x0), w[j], gq0);
-                        gq1 = ffma2(fmul2(g[j + 1], x1), w[j + 1], gq1);
-                    }
-                    q0 = fadd2(q0, q1);
-                    gq0 = fadd2(gq0, gq1);
-                    float sums2[2] = {q0.x + q0.y, gq0.x + gq0.y};  // x^2, g w x
-                    th.row_sums(p, sums2);
-                    const float r = on ? row_rsqrt<T>(fmaf(sums2[0], inv_d, p.eps)) : 0.f;
-                    const float kx = -r * r * r * (sums2[1] * inv_d);
-                    const float2 r2 = make_float2(r, r), k2 = make_float2(kx, kx);
-                    Group<T> y;
+
+        // a position of the walk: unit un, passes [ps, p1) of it left
+        struct Walk {
+            int64_t un;
+            int b, s, ps, p1;
+        };
+        auto enter = [&](Walk& w) {  // the first unit from w.un on that has passes of this side
+            for (; w.un < units; w.un += step) {
+                const Unit u = unit_at(p, w.un);
+                w.b = u.b;
+                w.s = u.s;
+                w.ps = (int)((int64_t)p.passes[side] * u.part / p.units_per_token);
+                w.p1 = (int)((int64_t)p.passes[side] * (u.part + 1) / p.units_per_token);
+                if (w.ps < w.p1) return;
+            }
+        };
+        auto fetch = [&](const Walk& w, Group<T>& x, Group<T>& g) {
+            if (w.un >= units) return;
+            const int h = min(w.ps * per_pass + th.slot, H - 1);
+            x.load(token_row<T>(p.x[side], w.b, w.s) + h * p.x[side].sh, th.at);
+            g.load(token_row<T>(p.g[side], w.b, w.s) + h * p.g[side].sh, th.at);
+        };
+        Walk ld{first, 0, 0, 0, 0};
+        enter(ld);
+        Group<T> xn, gn;
+        fetch(ld, xn, gn);
+        // interleaved: cos, sin of pair j; half: cos of pairs 2j, 2j + 1, then
+        // their sines; shifted: cos of elements 2j, 2j + 1, then their signed sines
+        float2 c[kStyle == kShifted ? 16 : 8];
+        int64_t angles_of = -1;
+        while (ld.un < units) {
+            const Walk cu = ld;
+            const Group<T> x = xn, gr = gn;
+            if (++ld.ps == ld.p1) {
+                ld.un += step;
+                enter(ld);
+            }
+            fetch(ld, xn, gn);
+            if (cu.un != angles_of) {
+                angles_of = cu.un;
+                token_angles<true>(p, Unit{cu.b, cu.s, 0}, cs);
+                if constexpr (kStyle == kShifted) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const float2 x = raw[i].two(j), gj = fmul2(g[j], r2);
-                        dw[j] = ffma2(gj, x, dw[j]);
-                        y.set(j, ffma2(gj, w[j], fmul2(x, k2)));
+                        const float2 a0 = th.angle_of(p, cs, th.group * 16 + 2 * j);
+                        const float2 a1 = th.angle_of(p, cs, th.group * 16 + 2 * j + 1);
+                        c[j] = make_float2(a0.x, a1.x);
+                        c[8 + j] = make_float2(-a0.y, -a1.y);  // the transposed rotation
                     }
-                    if (on && th.live) y.store(yt + h * p.y[side].sh, th.at);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 a = th.angles(p, cs, j);
+                        c[kStyle == kInter ? 2 * j : j] = kStyle == kInter ? make_float2(a.x, a.y) : make_float2(a.x, a.z);
+                        c[kStyle == kInter ? 2 * j + 1 : 4 + j] = kStyle == kInter ? make_float2(a.z, a.w) : make_float2(a.y, a.w);
+                    }
                 }
             }
+            const int h = cu.ps * per_pass + th.slot;
+            const bool on = h < H;
+            float2 g[8];
+            if constexpr (kStyle == kShifted) {
+                pt.put(gr);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    g[j] = ffma2(gr.two(j), c[j], fmul2(pt.pair(p, th.group * 16 + 2 * j, th.lane0), c[8 + j]));
+            } else if constexpr (kStyle == kInter) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 v = gr.two(j);
+                    g[j] = make_float2(fmaf(v.x, c[j].x, v.y * c[j].y), fmaf(v.y, c[j].x, -(v.x * c[j].y)));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 g1 = gr.two(j), g2 = gr.two(4 + j);
+                    g[j] = ffma2(g1, c[j], fmul2(g2, c[4 + j]));
+                    g[4 + j] = fsub2(fmul2(g2, c[j]), fmul2(g1, c[4 + j]));
+                }
+            }
+            float2 q0 = make_float2(0.f, 0.f), q1 = q0, gq0 = q0, gq1 = q0;
+            float2 gw[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float2 x0 = x.two(j), x1 = x.two(j + 1);
+                const float4 w = ws[j / 2][th.group];
+                gw[j] = fmul2(g[j], make_float2(w.x, w.y));
+                gw[j + 1] = fmul2(g[j + 1], make_float2(w.z, w.w));
+                q0 = ffma2(x0, x0, q0);
+                q1 = ffma2(x1, x1, q1);
+                gq0 = ffma2(gw[j], x0, gq0);
+                gq1 = ffma2(gw[j + 1], x1, gq1);
+            }
+            q0 = fadd2(q0, q1);
+            gq0 = fadd2(gq0, gq1);
+            float sums2[2] = {q0.x + q0.y, gq0.x + gq0.y};  // x^2, g w x
+            th.row_sums(p, sums2);
+            const float r = on ? row_rsqrt<T>(fmaf(sums2[0], inv_d, p.eps)) : 0.f;
+            const float kx = -r * r * r * (sums2[1] * inv_d);
+            const float2 r2 = make_float2(r, r), k2 = make_float2(kx, kx);
+            Group<T> y;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 xj = x.two(j);
+                dw[j] = ffma2(fmul2(g[j], r2), xj, dw[j]);
+                y.set(j, ffma2(gw[j], r2, fmul2(xj, k2)));
+            }
+            if (on && th.live) y.store(token_row<T>(p.y[side], cu.b, cu.s) + h * p.y[side].sh, th.at);
         }
         if (p.dw_part) {
             // over the warp's heads, then over the block's warps, in a fixed order
@@ -705,27 +733,25 @@ cudaError_t launch_rope_mode(const RopeParams& p, bool vec, unsigned grid, cudaS
     const int style = p.interleaved ? kInter : p.rot % 16 == 0 ? kHalf : kShifted;
     if (!vec) return launch_kernel(false, rope_pairs_kernel<T, kMode>, dim3(grid), gblk, 0, s, p);
     if constexpr (kMode == kNormGrad) {
-        // one pass and four blocks (254 us on 32760 tokens of 24/24 heads, D = 128;
-        // two passes and three blocks 260): warps hide the loads, registers do not
-        constexpr int kBatch = 1;
-        auto kern = style == kInter ? norm_grad_kernel<T, kInter, kBatch, kGradBlocks>
-                    : style == kHalf ? norm_grad_kernel<T, kHalf, kBatch, kGradBlocks>
-                                     : norm_grad_kernel<T, kShifted, 1, kGradBlocksShifted>;
+        constexpr int kBlocks = sizeof(T) == 4 ? kGradBlocksWide : kGradBlocks;
+        auto kern = style == kInter ? norm_grad_kernel<T, kInter, kBlocks>
+                    : style == kHalf ? norm_grad_kernel<T, kHalf, kBlocks>
+                                     : norm_grad_kernel<T, kShifted, kGradBlocksWide>;
         return launch_kernel(false, kern, dim3(grid), gblk, 0, s, p);
     } else {
         // Passes in flight against warps on an SM.  The norm's six (the longest
-        // batch that does not spill at two blocks) took 138 us on 32760 tokens
-        // of 24/24 heads, D = 128, two at three blocks 143; rows of fewer passes
+        // batch that does not spill at 16 warps) took 127 us on 32760 tokens
+        // of 24/24 heads, D = 128, two at 24 warps 143; rows of fewer passes
         // have nothing to fill six with.
         constexpr bool kNormed = kMode == kNorm;
-        constexpr int kLong = sizeof(T) == 4 ? 2 : kNormed ? 6 : 3, kLongBlocks = kNormed ? 2 : 3;
-        constexpr int kShort = 2, kShortBlocks = 3;
+        constexpr int kLong = sizeof(T) == 4 ? 2 : kNormed ? 6 : 3, kLongBlocks = kNormed ? 8 : 12;
+        constexpr int kShort = 2, kShortBlocks = 12;
         const bool few = kNormed && std::max(p.passes[0], p.passes[1]) <= 3;
         auto kern = style == kInter ? (few ? rope_kernel<T, kInter, kNormed, kShort, kShortBlocks>
                                            : rope_kernel<T, kInter, kNormed, kLong, kLongBlocks>)
                     : style == kHalf ? (few ? rope_kernel<T, kHalf, kNormed, kShort, kShortBlocks>
                                             : rope_kernel<T, kHalf, kNormed, kLong, kLongBlocks>)
-                                     : rope_kernel<T, kShifted, kNormed, kShort, 2>;
+                                     : rope_kernel<T, kShifted, kNormed, kShort, 8>;
         return launch_kernel(false, kern, dim3(grid), blk, 0, s, p);
     }
 }
@@ -839,8 +865,8 @@ int rope_call(const char* name, int mode, const ctx_tensor_t* const x[2], const 
     const bool walk = mode == kNormGrad || !vec;  // kernels whose warps walk many units
     const int warps = walk ? kGradWarps : kWarps;
     int64_t grid = (units + warps - 1) / warps;
-    const bool shifted = !p.interleaved && p.rot % 16 != 0;
-    const int64_t per_sm = !vec ? 16 : shifted ? kGradBlocksShifted : kGradBlocks;
+    const bool wide = size == 4 || (!p.interleaved && p.rot % 16 != 0);
+    const int64_t per_sm = !vec ? 16 : wide ? kGradBlocksWide : kGradBlocks;
     if (walk) grid = std::min<int64_t>(grid, std::min<int64_t>(per_sm * sms, kMaxGradBlocks));
     if (grid > INT32_MAX) return CTX_ERR_INVALID_ARG;
     const bool want_dw = mode == kNormGrad && (p.dw[0] || p.dw[1]);
