@@ -193,7 +193,7 @@ _HERE = contextlib.nullcontext()
 
 def _on(device):
     """Makes `device` current for a launch when it is not."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _raw_stream(device):
@@ -207,10 +207,8 @@ def _packed(t, name, dtype, device):
         raise ValueError(f"{name}: expected a logical [B,S,H,D] tensor, got {len(shape)} dims")
     if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: tensor must be on a CUDA device")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the other tensors are on {device}")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name}: on {t.device}; every tensor must be on one CUDA device")
     if stride[3] != 1:
         raise ValueError(f"{name}: the D dimension must be contiguous")
     return _PACK(t.data_ptr(), *shape, *stride[:3])
@@ -221,16 +219,17 @@ def _result(given, name, like):
     `like`'s type, shape and storage order."""
     if given is not None:
         return given, _packed(given, name, like.dtype, like.device)
-    shape, stride = like.shape, like.stride()
-    if like.is_contiguous():
-        t = torch.empty_like(like)
-        return t, _PACK(t.data_ptr(), *shape, *stride[:3])
-    B, S, H, D = shape
+    B, S, H, D = shape = like.shape
+    stride = like.stride()
     if stride[0] >= stride[1]:  # [B,S,H,D] storage
-        t = torch.empty((B, S, H, D), dtype=like.dtype, device=like.device)
-        return t, _PACK(t.data_ptr(), B, S, H, D, S * H * D, H * D, D)
-    t = torch.empty((S, B, H, D), dtype=like.dtype, device=like.device).permute(1, 0, 2, 3)
-    return t, _PACK(t.data_ptr(), B, S, H, D, H * D, B * H * D, D)
+        dense = (S * H * D, H * D, D, 1)
+    else:
+        dense = (H * D, B * H * D, D, 1)
+    if stride == dense:
+        t = torch.empty_like(like)
+    else:
+        t = torch.empty_strided(shape, dense, dtype=like.dtype, device=like.device)
+    return t, _PACK(t.data_ptr(), B, S, H, D, *dense[:3])
 
 
 def _lse(given, B, H, S, device):
@@ -592,7 +591,7 @@ def _rope_desc(table, positions, offset, B, S, device):
         if axes > 1:
             raise ValueError("a table with several position axes needs positions")
         return _PACK_ROPE(*table._head, 0, 0, 0, 0, int(offset))
-    if positions.dtype != torch.int64 or positions.device != device:
+    if positions.dtype is not torch.int64 or positions.device != device:
         raise ValueError(f"positions: expected int64 on {device}, got {positions.dtype} on {positions.device}")
     shape, stride = positions.shape, positions.stride()
     sa = 0
