@@ -3,7 +3,8 @@
 Every computation runs in the CUDA library ``_build/libctxattn.so`` through
 its C ABI (``include/ctx_attn.h``); this module only marshals torch tensors
 into ``ctx_tensor_t`` descriptors, allocates outputs and workspace with torch,
-and passes the current CUDA stream.  There is no CPU path: if the library is
+and passes the current CUDA stream.  The windowed, decoding, rotary and norm
+calls do that part natively (``csrc/binding.cpp``), the others with ctypes.  There is no CPU path: if the library is
 missing or a call fails, an exception is raised.
 
 Tensors are *logical* ``[B, S, H, D]`` views (``.permute(1, 0, 2, 3)`` of a
@@ -12,9 +13,9 @@ library how they are stored.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
+import importlib.util
 import math
 import os
 import struct
@@ -40,6 +41,7 @@ DEBUG_SKIP_ARRIVAL = 1
 LAYOUT_BSHD, LAYOUT_SBHD = 0, 1
 _lock = threading.Lock()
 _lib = None
+_binding = None
 
 
 class CtxError(RuntimeError):
@@ -102,18 +104,18 @@ def load_library(build_if_missing: bool = True):
             lib.ctx_attn_launch_plan.argtypes = [I, I, I, I, I, I, P(I), I, P(_Plan)]
             lib.ctx_debug_set.argtypes = [ctypes.c_uint, ctypes.c_uint]
             lib.ctx_kernel_binary_version.argtypes = [P(I)]
-            # descriptors of the calls below are passed packed (bytes), see _PACK
-            lib.ctx_attn_window_fwd.argtypes = [V, V, V, I, P(I), I, I, I, I, I, F, V, V, V]
-            lib.ctx_attn_window_bwd.argtypes = [V, V, V, V, V, V, I, P(I), I, I, I, I, I, F, V, V, V, V, SZ, V]
+            R = P(_Rope)
+            lib.ctx_attn_window_fwd.argtypes = [T, T, T, I, P(I), I, I, I, I, I, F, T, V, V]
+            lib.ctx_attn_window_bwd.argtypes = [T, T, T, T, V, T, I, P(I), I, I, I, I, I, F, T, T, T, V, SZ, V]
             lib.ctx_attn_window_workspace_size.argtypes = [I] * 10
             lib.ctx_attn_window_workspace_size.restype = SZ
-            lib.ctx_attn_decode.argtypes = [V, V, V, V, I, I, I, F, V, V, V, SZ, V]
+            lib.ctx_attn_decode.argtypes = [T, T, T, V, I, I, I, F, T, V, V, SZ, V]
             lib.ctx_attn_decode_workspace_size.argtypes = [I] * 8
             lib.ctx_attn_decode_workspace_size.restype = SZ
-            lib.ctx_rope_fwd.argtypes = [V, V, V, I, I, V, V, V]
-            lib.ctx_rope_bwd.argtypes = [V, V, V, I, I, V, V, V]
-            lib.ctx_qk_norm_rope_fwd.argtypes = [V, V, V, V, I, F, V, I, I, V, V, V]
-            lib.ctx_qk_norm_rope_bwd.argtypes = [V, V, V, V, V, V, I, F, V, I, I, V, V, V, V, V, SZ, V]
+            lib.ctx_rope_fwd.argtypes = [T, T, R, I, I, T, T, V]
+            lib.ctx_rope_bwd.argtypes = [T, T, R, I, I, T, T, V]
+            lib.ctx_qk_norm_rope_fwd.argtypes = [T, T, V, V, I, F, R, I, I, T, T, V]
+            lib.ctx_qk_norm_rope_bwd.argtypes = [T, T, T, T, V, V, I, F, R, I, I, T, T, V, V, V, SZ, V]
             lib.ctx_qk_norm_rope_workspace_size.argtypes = [I]
             lib.ctx_qk_norm_rope_workspace_size.restype = SZ
             lib.ctx_status_string.argtypes = [I]
@@ -127,6 +129,29 @@ def load_library(build_if_missing: bool = True):
                 getattr(lib, n).restype = I
             _lib = lib
     return _lib
+
+
+def _native():
+    """The module that marshals torch tensors for the calls below (csrc/binding.cpp)."""
+    global _binding
+    if _binding is None:
+        load_library()
+        with _lock:
+            if _binding is None:
+                if not os.path.exists(_build.BINDING):
+                    raise RuntimeError(f"binding not built: {_build.BINDING} (run build())")
+                spec = importlib.util.spec_from_file_location(__name__ + "._binding", _build.BINDING)
+                mod = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(mod)
+                _binding = mod
+    return _binding
+
+
+def _done(answer, what: str):
+    """The results of a native call, or the error its status code stands for."""
+    if type(answer) is int:
+        raise CtxError(answer, what)
+    return answer
 
 
 def _status_text(code: int) -> str:
@@ -183,79 +208,6 @@ def _check_inputs(named, device, lse=None, lse_shape=None):
             raise ValueError(f"{name}: on {t.device}, the other tensors are on {device}")
 
 
-# ctx_tensor_t and ctx_rope_t in the C compiler's layout.  Short calls (one new
-# token) are bound by the host: a packed descriptor costs a fraction of a
-# ctypes structure.
-_PACK = struct.Struct("P7q").pack
-_PACK_ROPE = struct.Struct("P3i4ifP4q").pack
-_HERE = contextlib.nullcontext()
-
-
-def _on(device):
-    """Makes `device` current for a launch when it is not."""
-    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
-
-
-def _raw_stream(device):
-    return torch._C._cuda_getCurrentRawStream(device.index)  # of torch.cuda.current_stream, without the object
-
-
-def _packed(t, name, dtype, device):
-    """ctx_tensor_t of a logical [B,S,H,D] tensor of this type and device."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 4:
-        raise ValueError(f"{name}: expected a logical [B,S,H,D] tensor, got {len(shape)} dims")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: dtype must be {dtype}, got {t.dtype}")
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name}: on {t.device}; every tensor must be on one CUDA device")
-    if stride[3] != 1:
-        raise ValueError(f"{name}: the D dimension must be contiguous")
-    return _PACK(t.data_ptr(), *shape, *stride[:3])
-
-
-def _result(given, name, like):
-    """(tensor, descriptor) of a result: the one given, or a new one of
-    `like`'s type, shape and storage order."""
-    if given is not None:
-        return given, _packed(given, name, like.dtype, like.device)
-    B, S, H, D = shape = like.shape
-    stride = like.stride()
-    if stride[0] >= stride[1]:  # [B,S,H,D] storage
-        dense = (S * H * D, H * D, D, 1)
-    else:
-        dense = (H * D, B * H * D, D, 1)
-    if stride == dense:
-        t = torch.empty_like(like)
-    else:
-        t = torch.empty_strided(shape, dense, dtype=like.dtype, device=like.device)
-    return t, _PACK(t.data_ptr(), B, S, H, D, *dense[:3])
-
-
-def _lse(given, B, H, S, device):
-    if given is None:
-        return torch.empty((B, H, S), dtype=torch.float32, device=device)
-    if (given.dtype != torch.float32 or tuple(given.shape) != (B, H, S) or not given.is_contiguous()
-            or given.device != device):
-        raise ValueError(f"lse: expected a contiguous float32 tensor of shape {(B, H, S)} on {device}, "
-                         f"got {given.dtype} {tuple(given.shape)} on {given.device}")
-    return given
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _scratch(nbytes, device, given):
-    """(pointer, bytes, tensor) of a call's workspace: the one given, or a new one."""
-    if given is None:
-        t = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-        return _ptr(t), nbytes, t
-    if given.device != device or not given.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on {device}, got one on {given.device}")
-    return given.data_ptr(), given.numel() * given.element_size(), given
-
-
 def _stream(t: torch.Tensor):
     return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
@@ -267,6 +219,10 @@ def _offsets(P, offsets):
     if len(off) != P + 1:
         raise ValueError("chunk offsets need P+1 entries")
     return (ctypes.c_int * (P + 1))(*off)
+
+
+def _offset_bytes(P, offsets):
+    return None if offsets is None else bytes(_offsets(P, offsets))
 
 
 def _like_layout(t: torch.Tensor, H: int) -> torch.Tensor:
@@ -376,35 +332,17 @@ def attn_window_fwd(q, k, v, P, window, sinks=0, chunk_offsets=None, causal=Fals
     .. i + right (-1: unlimited; causal: nothing after i), and the first
     ``sinks`` keys of the sequence.  A causal window of W tokens, the query's
     own among them, is (W - 1, 0)."""
-    lib, dev, bf = load_library(), q.device, torch.bfloat16
     left, right, sinks = _window(window, sinks)
-    dq, dk, dv = _packed(q, "q", bf, dev), _packed(k, "k", bf, dev), _packed(v, "v", bf, dev)
-    out, do = _result(out, "out", q)
-    lse = _lse(lse, q.shape[0], q.shape[2], q.shape[1], dev)
-    with _on(dev):
-        rc = lib.ctx_attn_window_fwd(dq, dk, dv, P, _offsets(P, chunk_offsets), LAYOUT_BSHD, int(causal), left, right,
-                                     sinks, float(scale) if scale else 0.0, do, lse.data_ptr(), _raw_stream(dev))
-    _check(rc, "ctx_attn_window_fwd")
-    return out, lse
+    return _done(_native().window_fwd(q, k, v, P, _offset_bytes(P, chunk_offsets), bool(causal), left, right, sinks,
+                                      scale or 0.0, out, lse), "ctx_attn_window_fwd")
 
 
 def attn_window_bwd(q, k, v, out, lse, dout, P, window, sinks=0, chunk_offsets=None, causal=False, scale=None,
                     dq=None, dk=None, dv=None, workspace=None):
     """Gradients through ``attn_window_fwd`` -> (dq, dk, dv) bf16, stored like q / k."""
-    lib, dev, bf = load_library(), q.device, torch.bfloat16
     left, right, sinks = _window(window, sinks)
-    ins = [_packed(t, n, bf, dev) for n, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout))]
-    B, S, Hq, D = q.shape
-    lse = _lse(lse, B, Hq, S, dev)
-    (dq, pq), (dk, pk), (dv, pv) = _result(dq, "dq", q), _result(dk, "dk", k), _result(dv, "dv", k)
-    with _on(dev):
-        nbytes = lib.ctx_attn_window_workspace_size(B, S, Hq, k.shape[2], D, P, int(causal), left, right, sinks)
-        ws, wsb, _keep = _scratch(nbytes, dev, workspace)
-        rc = lib.ctx_attn_window_bwd(*ins[:4], lse.data_ptr(), ins[4], P, _offsets(P, chunk_offsets), LAYOUT_BSHD,
-                                     int(causal), left, right, sinks, float(scale) if scale else 0.0, pq, pk, pv,
-                                     ws, wsb, _raw_stream(dev))
-    _check(rc, "ctx_attn_window_bwd")
-    return dq, dk, dv
+    return _done(_native().window_bwd(q, k, v, out, lse, dout, P, _offset_bytes(P, chunk_offsets), bool(causal), left,
+                                      right, sinks, scale or 0.0, dq, dk, dv, workspace), "ctx_attn_window_bwd")
 
 
 def decode_workspace_size(B, T, Hq, Hkv, D, capacity, window=-1, sinks=0) -> int:
@@ -422,24 +360,8 @@ def attn_decode(q, k, v, lengths=None, window=-1, sinks=0, scale=None, out=None,
     full).  Query t is at position length - T + t; it sees the keys up to
     itself, of those the last ``window`` before it (-1: all) and the first
     ``sinks``.  A query before its sequence's start gives 0 and -inf."""
-    lib, dev, bf = load_library(), q.device, torch.bfloat16
-    _, _, sinks = _window((window, 0), sinks)
-    dq, dk, dv = _packed(q, "q", bf, dev), _packed(k, "k", bf, dev), _packed(v, "v", bf, dev)
-    B, T, Hq, D = q.shape
-    if lengths is not None and (lengths.dtype != torch.int32 or tuple(lengths.shape) != (B,)
-                                or not lengths.is_contiguous() or lengths.device != dev):
-        raise ValueError(f"lengths: expected a contiguous int32 tensor of shape {(B,)} on {dev}, "
-                         f"got {lengths.dtype} {tuple(lengths.shape)} on {lengths.device}")
-    out, do = _result(out, "out", q)
-    lse = _lse(lse, B, Hq, T, dev)
-    left = min(window, (1 << 31) - 1)
-    with _on(dev):
-        ws, wsb, _keep = _scratch(
-            lib.ctx_attn_decode_workspace_size(B, T, Hq, k.shape[2], D, k.shape[1], left, sinks), dev, workspace)
-        rc = lib.ctx_attn_decode(dq, dk, dv, _ptr(lengths), LAYOUT_BSHD, left, sinks, float(scale) if scale else 0.0,
-                                 do, lse.data_ptr(), ws, wsb, _raw_stream(dev))
-    _check(rc, "ctx_attn_decode")
-    return out, lse
+    left, _, sinks = _window((window, 0), sinks)
+    return _done(_native().decode(q, k, v, lengths, left, sinks, scale or 0.0, out, lse, workspace), "ctx_attn_decode")
 
 
 def exchanged_shape(B, S, H, D, ring, ulysses, layout):
@@ -490,7 +412,7 @@ def exchanged_view(y, S, layout):
 
 
 # ---------------------------------------------------------------- rotary positions, query/key norms
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_PACK_ROPE = struct.Struct("P3i4ifP4q").pack  # ctx_rope_t in the C compiler's layout
 
 
 @dataclass(frozen=True)
@@ -510,9 +432,16 @@ class RopeTable:
 
     @functools.cached_property
     def _head(self):
-        """The leading fields of ctx_rope_t."""
-        return (self.turns.data_ptr(), self.rot_dim, int(self.interleaved), len(self.sections),
-                *self.sections, *[0] * (4 - len(self.sections)), self.magnitude)
+        """ctx_rope_t without positions, as bytes."""
+        return _PACK_ROPE(self.turns.data_ptr(), self.rot_dim, int(self.interleaved), len(self.sections),
+                          *self.sections, *[0] * (4 - len(self.sections)), self.magnitude, 0, 0, 0, 0, 0)
+
+
+_NO_TABLE = (None, None)
+
+
+def _table(table):
+    return _NO_TABLE if table is None else (table._head, table.turns)
 
 
 def rope_table(rot_dim, theta=10000.0, interleaved=False, sections=None, scaling="none", factor=1.0,
@@ -578,62 +507,6 @@ def rope_table(rot_dim, theta=10000.0, interleaved=False, sections=None, scaling
                      float(magnitude))
 
 
-def _rope_desc(table, positions, offset, B, S, device):
-    """ctx_rope_t of a call (None without a table)."""
-    if table is None:
-        if positions is not None:
-            raise ValueError("positions given without a table")
-        return None
-    if table.turns.device != device:
-        raise ValueError(f"table: on {table.turns.device}, the tensors are on {device}")
-    axes = len(table.sections)
-    if positions is None:
-        if axes > 1:
-            raise ValueError("a table with several position axes needs positions")
-        return _PACK_ROPE(*table._head, 0, 0, 0, 0, int(offset))
-    if positions.dtype is not torch.int64 or positions.device != device:
-        raise ValueError(f"positions: expected int64 on {device}, got {positions.dtype} on {positions.device}")
-    shape, stride = positions.shape, positions.stride()
-    sa = 0
-    if axes > 1:
-        if len(shape) < 2 or shape[-1] != axes:
-            raise ValueError(f"positions: expected [S, {axes}] or [B, S, {axes}], got {tuple(shape)}")
-        shape, stride, sa = shape[:-1], stride[:-1], stride[-1]
-    if len(shape) == 1 and shape[0] == S:
-        sb, ss = 0, stride[0]
-    elif len(shape) == 2 and shape[0] in (1, B) and shape[1] == S:
-        sb, ss = (0 if shape[0] == 1 else stride[0]), stride[1]
-    else:
-        raise ValueError(f"positions: {tuple(positions.shape)} does not fit {B} sequences of {S} tokens")
-    return _PACK_ROPE(*table._head, positions.data_ptr(), sb, ss, sa, 0)
-
-
-def _row_type(t, name):
-    if t.dim() != 4:
-        raise ValueError(f"{name}: expected a logical [B,S,H,D] tensor, got {t.dim()} dims")
-    dtype = _DTYPES.get(t.dtype)
-    if dtype is None:
-        raise ValueError(f"{name}: dtype must be bfloat16, float16 or float32, got {t.dtype}")
-    return dtype
-
-
-def _rotate(entry, names, a, b, table, positions, offset, a_out, b_out):
-    lib = load_library()
-    if table is None:
-        raise ValueError("table: a RopeTable is required")
-    dtype, dev, dt = a.dtype, a.device, _row_type(a, names[0])
-    pa, pb = _packed(a, names[0], dtype, dev), None if b is None else _packed(b, names[1], dtype, dev)
-    rope = _rope_desc(table, positions, offset, a.shape[0], a.shape[1], dev)
-    a_out, qa = _result(a_out, names[2], a)
-    qb = None
-    if b is not None:
-        b_out, qb = _result(b_out, names[3], b)
-    with _on(dev):
-        rc = getattr(lib, entry)(pa, pb, rope, dt, LAYOUT_BSHD, qa, qb, _raw_stream(dev))
-    _check(rc, entry)
-    return a_out, b_out
-
-
 def rope_fwd(q, k, table, positions=None, offset=0, q_out=None, k_out=None):
     """Rotary positions -> (q_out, k_out), stored like q and k (k may be None).
 
@@ -641,25 +514,12 @@ def rope_fwd(q, k, table, positions=None, offset=0, q_out=None, k_out=None):
     or [B,S] ([S,axes] or [B,S,axes] for a table with several axes); without
     it token s of every sequence is at ``offset + s``.  q_out / k_out may be
     q / k."""
-    return _rotate("ctx_rope_fwd", ("q", "k", "q_out", "k_out"), q, k, table, positions, offset, q_out, k_out)
+    return _done(_native().rotate(0, *_table(table), q, k, positions, offset, q_out, k_out), "ctx_rope_fwd")
 
 
 def rope_bwd(dq_out, dk_out, table, positions=None, offset=0, dq=None, dk=None):
     """Gradients through ``rope_fwd`` -> (dq, dk): the transposed rotation."""
-    return _rotate("ctx_rope_bwd", ("dq_out", "dk_out", "dq", "dk"), dq_out, dk_out, table, positions, offset, dq, dk)
-
-
-def _weight_type(wq, wk, D, device):
-    dt = None
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is None:
-            continue
-        if w.shape != (D,) or not w.is_contiguous() or w.device != device or w.dtype not in _DTYPES:
-            raise ValueError(f"{name}: expected a contiguous [{D}] tensor on {device}, got {w.dtype} {tuple(w.shape)}")
-        if dt is not None and w.dtype != dt:
-            raise ValueError(f"{name}: both weights must have one dtype")
-        dt = w.dtype
-    return 2 if dt is None else _DTYPES[dt]
+    return _done(_native().rotate(1, *_table(table), dq_out, dk_out, positions, offset, dq, dk), "ctx_rope_bwd")
 
 
 def qk_norm_rope_fwd(q, k, wq, wk, table, positions=None, offset=0, eps=1e-6, q_out=None, k_out=None):
@@ -668,20 +528,8 @@ def qk_norm_rope_fwd(q, k, wq, wk, table, positions=None, offset=0, eps=1e-6, q_
 
     wq, wk: [D] weights or None (ones); table None: the norm alone; the other
     arguments as in ``rope_fwd``."""
-    lib = load_library()
-    dtype, dev, dt = q.dtype, q.device, _row_type(q, "q")
-    pq, pk = _packed(q, "q", dtype, dev), None if k is None else _packed(k, "k", dtype, dev)
-    wt = _weight_type(wq, wk, q.shape[3], dev)
-    rope = _rope_desc(table, positions, offset, q.shape[0], q.shape[1], dev)
-    q_out, oq = _result(q_out, "q_out", q)
-    ok = None
-    if k is not None:
-        k_out, ok = _result(k_out, "k_out", k)
-    with _on(dev):
-        rc = lib.ctx_qk_norm_rope_fwd(pq, pk, _ptr(wq), _ptr(wk), wt, eps, rope, dt, LAYOUT_BSHD, oq, ok,
-                                      _raw_stream(dev))
-    _check(rc, "ctx_qk_norm_rope_fwd")
-    return q_out, k_out
+    return _done(_native().norm_fwd(*_table(table), q, k, wq, wk, positions, offset, eps, q_out, k_out),
+                 "ctx_qk_norm_rope_fwd")
 
 
 def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, table, positions=None, offset=0, eps=1e-6, dq=None, dk=None,
@@ -690,33 +538,8 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, wq, wk, table, positions=None, offset
 
     q, k are the forward's inputs; nothing else is saved.  dwq, dwk: fp32 [D]
     (None for a weight that is None), summed in a fixed order."""
-    lib = load_library()
-    if (k is None) != (dk_out is None):
-        raise ValueError("k and dk_out go together")
-    dtype, dev, dt = q.dtype, q.device, _row_type(q, "q")
-    pq, pg = _packed(q, "q", dtype, dev), _packed(dq_out, "dq_out", dtype, dev)
-    pk = ph = ok = None
-    if k is not None:
-        pk, ph = _packed(k, "k", dtype, dev), _packed(dk_out, "dk_out", dtype, dev)
-    D = q.shape[3]
-    wt = _weight_type(wq, wk, D, dev)
-    for name, g, w in (("dwq", dwq, wq), ("dwk", dwk, wk)):
-        if g is not None and (w is None or g.dtype != torch.float32 or tuple(g.shape) != (D,)
-                              or not g.is_contiguous() or g.device != dev):
-            raise ValueError(f"{name}: expected a contiguous float32 [{D}] tensor on {dev}, beside its weight")
-    rope = _rope_desc(table, positions, offset, q.shape[0], q.shape[1], dev)
-    dq, oq = _result(dq, "dq", q)
-    if k is not None:
-        dk, ok = _result(dk, "dk", k)
-    dwq = torch.empty(D, dtype=torch.float32, device=dev) if dwq is None and wq is not None else dwq
-    dwk = torch.empty(D, dtype=torch.float32, device=dev) if dwk is None and wk is not None else dwk
-    need = lib.ctx_qk_norm_rope_workspace_size(D) if dwq is not None or dwk is not None else 0
-    ws, wsb, _keep = _scratch(need, dev, workspace)
-    with _on(dev):
-        rc = lib.ctx_qk_norm_rope_bwd(pg, ph, pq, pk, _ptr(wq), _ptr(wk), wt, eps, rope, dt, LAYOUT_BSHD, oq, ok,
-                                      _ptr(dwq), _ptr(dwk), ws, wsb, _raw_stream(dev))
-    _check(rc, "ctx_qk_norm_rope_bwd")
-    return dq, dk, dwq, dwk
+    return _done(_native().norm_bwd(*_table(table), dq_out, dk_out, q, k, wq, wk, positions, offset, eps, dq, dk, dwq,
+                                    dwk, workspace), "ctx_qk_norm_rope_bwd")
 
 
 def device_status(stream=None) -> int:
