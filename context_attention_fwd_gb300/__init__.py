@@ -4,8 +4,9 @@ Every computation runs in the CUDA library ``_build/libctxattn.so`` through
 its C ABI (``include/ctx_attn.h``); this module only marshals torch tensors
 into ``ctx_tensor_t`` descriptors, allocates outputs and workspace with torch,
 and passes the current CUDA stream.  The windowed, decoding, rotary and norm
-calls do that part natively (``csrc/binding.cpp``), the others with ctypes.  There is no CPU path: if the library is
-missing or a call fails, an exception is raised.
+calls do that part natively (``csrc/binding.cpp``), the others with ctypes.
+There is no CPU path: if the library is missing or a call fails, an exception
+is raised.
 
 Tensors are *logical* ``[B, S, H, D]`` views (``.permute(1, 0, 2, 3)`` of a
 sequence-first ``[S, B, H, D]`` tensor is one); their strides tell the

@@ -105,10 +105,11 @@ ctx_stream_t stream_of(c10::Device dev) {
     return reinterpret_cast<ctx_stream_t>(c10::cuda::getCurrentCUDAStream(dev.index()).stream());
 }
 
-long as_long(PyObject* o) {
+int as_int(PyObject* o, const char* name) {
     const long v = PyLong_AsLong(o);
     if (v == -1 && PyErr_Occurred()) throw python_error();
-    return v;
+    if (v < INT32_MIN || v > INT32_MAX) refuse(name, ": ", v, " does not fit 32 bits");
+    return (int)v;
 }
 double as_double(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
@@ -209,7 +210,7 @@ PyObject* answer(int rc, std::initializer_list<Tensor> ts) { return rc ? PyLong_
 
 // backward, head, turns, a, b, positions, offset, a_out, b_out
 PyObject* rotate(PyObject* const* a) {
-    const bool back = as_long(a[0]) != 0;
+    const bool back = as_int(a[0], "backward") != 0;
     const char *na = back ? "dq_out" : "q", *nb = back ? "dk_out" : "k", *noa = back ? "dq" : "q_out",
                *nob = back ? "dk" : "k_out";
     const Tensor& x = tensor(a[3], na);
@@ -314,8 +315,8 @@ PyObject* window_fwd(PyObject* const* a) {
     const c10::Device dev = q.device();
     const ctx_tensor_t dq = describe(q, "q", at::kBFloat16, dev), dk = describe(k, "k", at::kBFloat16, dev),
                        dv = describe(v, "v", at::kBFloat16, dev);
-    const int P = (int)as_long(a[3]), causal = (int)as_long(a[5]), left = (int)as_long(a[6]), right = (int)as_long(a[7]),
-              sinks = (int)as_long(a[8]);
+    const int P = as_int(a[3], "P"), causal = as_int(a[5], "causal"), left = as_int(a[6], "window"),
+              right = as_int(a[7], "window"), sinks = as_int(a[8], "sinks");
     const float scale = (float)as_double(a[9]);
     const c10::cuda::CUDAGuard guard(dev);
     ctx_tensor_t od;
@@ -339,8 +340,8 @@ PyObject* window_bwd(PyObject* const* a) {
                        tg = describe(tensor(a[5], "dout"), "dout", at::kBFloat16, dev);
     if (!given(a[4])) refuse("lse: expected the forward's");
     const Tensor lse = lse_result(a[4], q.size(0), q.size(2), q.size(1), dev);
-    const int P = (int)as_long(a[6]), causal = (int)as_long(a[8]), left = (int)as_long(a[9]), right = (int)as_long(a[10]),
-              sinks = (int)as_long(a[11]);
+    const int P = as_int(a[6], "P"), causal = as_int(a[8], "causal"), left = as_int(a[9], "window"),
+              right = as_int(a[10], "window"), sinks = as_int(a[11], "sinks");
     const float scale = (float)as_double(a[12]);
     const c10::cuda::CUDAGuard guard(dev);
     ctx_tensor_t oq, ok, ov;
@@ -372,7 +373,7 @@ PyObject* decode(PyObject* const* a) {
                    n.scalar_type(), " ", n.sizes(), " on ", n.device());
         lengths = static_cast<const int*>(n.data_ptr());
     }
-    const int left = (int)as_long(a[4]), sinks = (int)as_long(a[5]);
+    const int left = as_int(a[4], "window"), sinks = as_int(a[5], "sinks");
     const float scale = (float)as_double(a[6]);
     const c10::cuda::CUDAGuard guard(dev);
     ctx_tensor_t od;

@@ -597,7 +597,7 @@ int sink_parts_cap(const Window& w, int ntiles) {
 // the CTAs in launch order, each on the first SM that is free, each with its
 // walk and about three iterations to start and end; summing partial rows adds
 // the time of their traffic.
-double win_split_time(const BwdParams& p, int D, int hs, int parts, int per, int head_major, int nsm) {
+double win_split_time(const BwdParams& p, int D, int hs, int parts, int per, int nsm) {
     std::vector<double> work;  // of the CTAs of one (head, z), in tile order
     const int G = p.group / hs;
     for (int i = 0; i < win_grid(p.ct.ntiles, p.sink_tiles, parts); ++i) {
@@ -614,13 +614,8 @@ double win_split_time(const BwdParams& p, int D, int hs, int parts, int per, int
         sm.back() += w;
         std::push_heap(sm.begin(), sm.end(), std::greater<double>());
     };
-    if (head_major) {
-        for (double w : work)
-            for (int64_t j = 0; j < other; ++j) run(w);
-    } else {
-        for (int64_t j = 0; j < other; ++j)
-            for (double w : work) run(w);
-    }
+    for (double w : work)
+        for (int64_t j = 0; j < other; ++j) run(w);
     const double span = *std::max_element(sm.begin(), sm.end());
     // partial rows: D * 8 bytes written and read, against some 3 us an iteration
     const double rows = (hs > 1 ? (double)hs * p.S : 0.0) + (hs * parts > 1 ? (double)hs * parts * p.sink_rows : 0.0);
@@ -629,13 +624,12 @@ double win_split_time(const BwdParams& p, int D, int hs, int parts, int per, int
 
 // The cut a call uses: the one of smallest estimated time, among the divisors
 // of the group size and the numbers of parts up to their most (ties to the
-// fewer pieces).  Long calls have CTAs enough: there the heads are not split.  Memoised: the estimate
-// runs on the host.
+// fewer pieces).  Long calls have CTAs enough: there the heads are not split.
+// Memoised: the estimate runs on the host.
 void plan_window_bwd(BwdParams* p, int D) {
     const int nt = p->ct.ntiles, S = p->S;
     p->hsplit = p->sink_parts = 1;
     p->sink_tiles = p->sink_rows = 0;
-    p->head_major = 1;
     if (p->win.sinks > 0) {
         p->sink_tiles = tile_of_row(p->ct, p->win.sinks - 1) + 1;
         const int last = p->sink_tiles - 1, c = chunk_of_tile(p->ct, last);
@@ -669,7 +663,7 @@ void plan_window_bwd(BwdParams* p, int D) {
             for (int hs = 1; hs <= hmax; ++hs) {
                 if (p->group % hs) continue;
                 for (int parts = 1; parts <= pmax; parts += std::max(1, pmax / 8)) {
-                    const double t = win_split_time(*p, D, hs, parts, per_of(parts), p->head_major, nsm);
+                    const double t = win_split_time(*p, D, hs, parts, per_of(parts), nsm);
                     if ((hs == 1 && parts == 1) || t < best) best = t, key.hs = hs, key.parts = parts;
                 }
             }
@@ -683,6 +677,9 @@ void plan_window_bwd(BwdParams* p, int D) {
     }
     if ((int64_t)p->B * 2 * p->hsplit > 65535) p->hsplit = 1;  // grid limit
     p->sink_per = per_of(p->sink_parts);
+    // heads first wherever the tiles fit the grid's z axis: at S = 4608, 24/8
+    // heads, D = 128, window 511 + 511 the call takes 217 us, tile by tile 238
+    p->head_major = win_grid(nt, p->sink_tiles, p->sink_parts) <= 65535;
 }
 
 size_t win_part_bytes(int B, int S, int Hq, int Hkv, int D, int hs) {

@@ -110,6 +110,24 @@ def test_random_windows(i, sh, left, right, sinks, causal, offsets):
     check(sh, left, right, sinks, causal, offsets=offsets)
 
 
+def test_more_tiles_than_a_grid_axis_holds():
+    """65538 KV tiles (a grid's y and z axes hold 65535) and offsets past
+    2^31 elements: the last rows against the definition on their own slab,
+    which under a causal window of 100 holds all they depend on."""
+    S, Hq, D, left, n, edge = 128 * 65537 + 5, 4, 64, 99, 512, 128
+    g = torch.Generator(device="cuda").manual_seed(11)
+    q, k, v, do = (torch.empty(1, S, h, D, device="cuda", dtype=torch.bfloat16).normal_(generator=g) for h in (Hq, 1, 1, Hq))
+    out, lse = ctx.attn_window_fwd(q, k, v, 1, (left, 0), causal=True)
+    grads = ctx.attn_window_bwd(q, k, v, out, lse, do, 1, (left, 0), causal=True)
+    a = S - n
+    slab = [t[:, a:].cpu() for t in (q, k, v, do)]
+    o_ref, l_ref = ref.attn_fwd(*slab[:3], left, 0, 0, True)
+    close("out", out[:, a + edge:], o_ref[:, edge:])
+    assert (lse[:, :, a + edge:].double().cpu() - l_ref[:, :, edge:]).abs().max() < 1e-3
+    for name, t, r in zip(("dq", "dk", "dv"), grads, ref.attn_bwd(*slab, left, 0, 0, True)):
+        close(name, t[:, a + edge:], r[:, edge:])
+
+
 def test_custom_scale():
     check(AttnShape(B=1, S=400, Hq=2, Hkv=2, D=128, P=2), 90, 0, 2, True, scale=0.2)
 
@@ -269,3 +287,13 @@ def test_refusals():
         ctx.attn_window_bwd(q, k, v, out, lse, q, 1, 5, workspace=torch.empty(1 << 24, dtype=torch.uint8))
     with pytest.raises(ValueError):
         ctx.attn_window_bwd(q, k, v, out, lse[:, :, :-1], q, 1, 5)
+
+
+def test_integers_past_32_bits_are_refused():
+    q = torch.randn(1, 8, 2, 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="32 bits"):
+        ctx.attn_window_fwd(q, q, q, (1 << 32) + 1, 4)
+    with pytest.raises(ValueError, match="expected a tensor"):
+        ctx.attn_window_fwd(q, q.tolist(), q, 1, 4)
+    out, _ = ctx.attn_window_fwd(q, q, q, 1, 1 << 40)  # a window may be any length
+    assert torch.equal(out, ctx.attn_window_fwd(q, q, q, 1, -1)[0])
