@@ -83,7 +83,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = BINDING + f".tmp{os.getpid()}"
     lib = os.path.join(torch_dir, "lib")
     r = subprocess.run(["g++", "-shared", "-o", tmp, binding, f"-L{BUILD}", "-lctxattn", f"-L{lib}", "-ltorch_python",
-                        "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], capture_output=True, text=True)
+                        "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)

@@ -13,9 +13,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
-#include <ATen/ops/empty_strided.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -55,6 +53,11 @@ ctx_tensor_t describe(const Tensor& t, const char* name, at::ScalarType type, c1
     return ctx_tensor_t{t.data_ptr(), t.size(0), t.size(1), t.size(2), t.size(3), t.stride(0), t.stride(1), t.stride(2)};
 }
 
+// Allocations go past torch's dispatcher, which has nothing to decide here.
+Tensor empty(at::IntArrayRef size, at::ScalarType type, c10::Device dev) {
+    return Tensor(at::detail::empty_cuda(size, type, dev, std::nullopt));
+}
+
 // A result: the tensor given, or a new one of `like`'s type, shape and storage order.
 Tensor result(PyObject* o, const char* name, const Tensor& like, ctx_tensor_t* d) {
     Tensor t;
@@ -62,17 +65,16 @@ Tensor result(PyObject* o, const char* name, const Tensor& like, ctx_tensor_t* d
         t = tensor(o, name);
     } else {
         const int64_t B = like.size(0), S = like.size(1), H = like.size(2), D = like.size(3);
-        if (like.stride(0) >= like.stride(1))
-            t = at::empty_strided({B, S, H, D}, {S * H * D, H * D, D, 1}, like.options());
-        else
-            t = at::empty_strided({B, S, H, D}, {H * D, B * H * D, D, 1}, like.options());
+        const bool bshd = like.stride(0) >= like.stride(1);
+        t = Tensor(at::detail::empty_strided_cuda({B, S, H, D}, {bshd ? S * H * D : H * D, bshd ? H * D : B * H * D, D, 1},
+                                                  like.scalar_type(), like.device()));
     }
     *d = describe(t, name, like.scalar_type(), like.device());
     return t;
 }
 
 Tensor lse_result(PyObject* o, int64_t B, int64_t H, int64_t S, c10::Device dev) {
-    if (!given(o)) return at::empty({B, H, S}, at::TensorOptions().dtype(at::kFloat).device(dev));
+    if (!given(o)) return empty({B, H, S}, at::kFloat, dev);
     const Tensor& t = tensor(o, "lse");
     if (t.scalar_type() != at::kFloat || t.dim() != 3 || t.size(0) != B || t.size(1) != H || t.size(2) != S ||
         !t.is_contiguous() || t.device() != dev)
@@ -94,7 +96,7 @@ Scratch scratch(PyObject* o, size_t need, c10::Device dev) {
             refuse("workspace: expected a contiguous tensor on ", dev, ", got one on ", s.t.device());
         s.bytes = s.t.nbytes();
     } else if (need) {
-        s.t = at::empty({(int64_t)need}, at::TensorOptions().dtype(at::kByte).device(dev));
+        s.t = empty({(int64_t)need}, at::kByte, dev);
         s.bytes = need;
     }
     if (s.t.defined()) s.p = s.t.data_ptr();
@@ -261,7 +263,7 @@ PyObject* norm_fwd(PyObject* const* a) {
 }
 
 Tensor weight_grad(PyObject* o, const char* name, PyObject* w, int64_t D, c10::Device dev) {
-    if (!given(o)) return given(w) ? at::empty({D}, at::TensorOptions().dtype(at::kFloat).device(dev)) : Tensor();
+    if (!given(o)) return given(w) ? empty({D}, at::kFloat, dev) : Tensor();
     const Tensor& t = tensor(o, name);
     if (!given(w) || t.scalar_type() != at::kFloat || t.dim() != 1 || t.size(0) != D || !t.is_contiguous() || t.device() != dev)
         refuse(name, ": expected a contiguous float32 [", D, "] tensor on ", dev, ", beside its weight");
