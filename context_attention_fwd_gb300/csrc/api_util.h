@@ -37,6 +37,16 @@ inline int num_sms() {
     return n > 0 ? n : 148;
 }
 
+// Whether a launch in the stream goes into a graph (or that cannot be told).
+inline bool stream_captured(cudaStream_t s) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+        cudaGetLastError();
+        return true;
+    }
+    return st != cudaStreamCaptureStatusNone;
+}
+
 struct Dense {
     void* data;
     int64_t sb, ss, sh;

@@ -507,12 +507,7 @@ int ctx_attn_decode(const ctx_tensor_t* q, const ctx_tensor_t* k, const ctx_tens
                 (long long)p.splits * p.Hkv * p.row_blocks * p.B);
     // the merge kernel's launch overlaps the first kernel, but not in a stream
     // that is being captured (replaying a graph removes the gap already)
-    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
-        cudaGetLastError();
-        st = cudaStreamCaptureStatusActive;
-    }
-    const bool pdl = st == cudaStreamCaptureStatusNone;
+    const bool pdl = !stream_captured(s);
     if (D == 64) return launch_decode<64>(p, pdl, s);
     if (D == 128) return launch_decode<128>(p, pdl, s);
     return launch_decode<256>(p, pdl, s);

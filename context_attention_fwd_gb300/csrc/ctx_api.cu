@@ -81,14 +81,15 @@ int pick_head_major(int causal, int64_t ctas) {
 // the D = 256 backward call (3-4% at 1536 tokens), which keeps plain
 // launches.  Replaying a CUDA graph already removes the gaps (and was slower
 // with it), so a stream that is being captured gets plain launches too.
-int use_pdl(int64_t ctas, int ntiles, cudaStream_t s) {
-    if (ctas * ntiles > 16LL * num_sms()) return 0;
-    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
-        cudaGetLastError();
-        return 0;
-    }
-    return st == cudaStreamCaptureStatusNone ? 1 : 0;
+//
+// A windowed backward has up to five kernels and CTAs of few steps each: it
+// gains up to 64 tile steps per SM, at D = 256 too (S = 4608, 24/8 heads,
+// D = 128, window 511 + 511: 217 -> 211 us; 1024 tokens of 24/4 heads,
+// D = 256, window 255: 92 -> 85 us; but S = 32760 at a window of 1024, 1667 ->
+// 1672 us).
+constexpr int kPdlSteps = 16, kPdlStepsWindowBwd = 64;
+int use_pdl(int64_t ctas, int ntiles, int steps, cudaStream_t s) {
+    return ctas * ntiles <= (int64_t)steps * num_sms() && !stream_captured(s) ? 1 : 0;
 }
 
 int build_chunks(int S, int P, const int* offsets, ChunkTable* ct) {
@@ -187,85 +188,92 @@ __global__ void exchange_kernel(const uint16_t* __restrict__ x, uint16_t* __rest
 // exactly 0 in the backward kernel.  Each thread also zeroes
 // eight values of the fp32 dQ accumulator (tile-major
 // [B][Hq][ntiles][D/4][128][4]), which the backward kernel adds into.
-__global__ void bwd_stats_kernel(const __nv_bfloat16* __restrict__ out, int64_t osb, int64_t oss,
-                                 int64_t osh, const __nv_bfloat16* __restrict__ dout, int64_t dsb,
-                                 int64_t dss, int64_t dsh, const float* __restrict__ lse,
-                                 float* __restrict__ nlse2_t, float* __restrict__ delta_t,
-                                 float* __restrict__ dq_acc, const ChunkTable ct, int Hq, int S, int D,
-                                 int64_t nslots) {
+//
+// A block has 256 threads, eight elements each of 2048 / D rows of one tile,
+// so where its tile lies is worked out once per block in 32 bits (per thread
+// in 64 bits that was most of the instructions: 20.8 instead of 16.8 us at
+// S = 4608, 24 heads, D = 128).
+template <int D>
+__global__ void __launch_bounds__(256) bwd_stats_kernel(
+    const __nv_bfloat16* __restrict__ out, int64_t osb, int64_t oss, int64_t osh,
+    const __nv_bfloat16* __restrict__ dout, int64_t dsb, int64_t dss, int64_t dsh, const float* __restrict__ lse,
+    float* __restrict__ nlse2_t, float* __restrict__ delta_t, float* __restrict__ dq_acc,
+    const __grid_constant__ ChunkTable ct, int Hq, int S) {
     griddep_wait();  // the previous kernel in the stream is complete (launch_kernel)
     griddep_launch_dependents();
-    const int tpr = D / 8;  // threads per row, 8 elements each
-    const int64_t gt = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t slot = gt / tpr;
-    const int part = (int)(gt - slot * tpr);
-    const bool in_range = slot < nslots;
-    const int64_t sl = in_range ? slot : 0;
-    const int rr = (int)(sl % kTile);
-    const int64_t bht = sl / kTile;
-    {
-        // zeroed in memory order, whatever rows the block has: its blockDim.x
-        // threads clear two float4 each of consecutive lines
-        float4* z4 = reinterpret_cast<float4*>(dq_acc) + (int64_t)blockIdx.x * blockDim.x * 2;
-        const int64_t end = nslots * (D / 4);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int64_t i = (int64_t)k * blockDim.x + threadIdx.x;
-            if ((int64_t)blockIdx.x * blockDim.x * 2 + i < end) z4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-    }
-    const int t = (int)(bht % ct.ntiles);
-    const int64_t bh = bht / ct.ntiles;
-    const int h = (int)(bh % Hq), b = (int)(bh / Hq);
+    constexpr int TPR = D / 8;  // threads per row, 8 elements each
+    constexpr int ROWS = 256 / TPR, PER_TILE = kTile / ROWS;
+    const uint32_t bht = blockIdx.x / PER_TILE, bh = bht / (uint32_t)ct.ntiles;
+    const int rr = (int)(blockIdx.x % PER_TILE) * ROWS + (int)threadIdx.x / TPR, part = threadIdx.x % TPR;
+    const int t = (int)(bht - bh * (uint32_t)ct.ntiles);
+    const int b = (int)(bh / (uint32_t)Hq), h = (int)(bh - (uint32_t)b * (uint32_t)Hq);
     const int c = chunk_of_tile(ct, t);
     const int s = ct.off[c] + (t - ct.tile_off[c]) * kTile + rr;
-    const bool valid = in_range && s < ct.off[c + 1];
-    float acc = 0.f;
+    const bool valid = s < ct.off[c + 1];
+    uint4 o = make_uint4(0, 0, 0, 0), g = o;
     if (valid) {
-        const uint4 o = *reinterpret_cast<const uint4*>(out + b * osb + (int64_t)s * oss + h * osh + part * 8);
-        const uint4 g = *reinterpret_cast<const uint4*>(dout + b * dsb + (int64_t)s * dss + h * dsh + part * 8);
-        const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&o);
-        const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&g);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 a = __bfloat1622float2(o2[k]), d = __bfloat1622float2(g2[k]);
-            acc = fmaf(a.x, d.x, acc);
-            acc = fmaf(a.y, d.y, acc);
-        }
+        o = *reinterpret_cast<const uint4*>(out + b * osb + (int64_t)s * oss + h * osh + part * 8);
+        g = *reinterpret_cast<const uint4*>(dout + b * dsb + (int64_t)s * dss + h * dsh + part * 8);
     }
-    for (int w = tpr / 2; w > 0; w >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, w, tpr);
-    if (in_range && part == 0) {
+    // zeroed in memory order, whatever rows the block has: two float4 a thread
+    // of consecutive lines
+    float4* z4 = reinterpret_cast<float4*>(dq_acc) + (int64_t)blockIdx.x * 512 + threadIdx.x;
+    z4[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    z4[256] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float acc = 0.f;
+    const __nv_bfloat162* o2 = reinterpret_cast<const __nv_bfloat162*>(&o);
+    const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&g);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 a = __bfloat1622float2(o2[k]), d = __bfloat1622float2(g2[k]);
+        acc = fmaf(a.x, d.x, acc);
+        acc = fmaf(a.y, d.y, acc);
+    }
+#pragma unroll
+    for (int w = TPR / 2; w > 0; w >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, w, TPR);
+    if (part == 0) {
+        const int64_t slot = (int64_t)bht * kTile + rr;
         delta_t[slot] = valid ? acc : 0.f;
         nlse2_t[slot] = valid ? -(lse[((int64_t)b * Hq + h) * S + s] * 1.4426950408889634f) : -INFINITY;
     }
 }
 
 // dq = scale * dq_acc, from tile-major fp32 [B][Hq][ntiles][D/4][128][4] to
-// bf16 rows of the caller's layout.  One thread per 8 columns of a row.
-__global__ void dq_convert_kernel(const float* __restrict__ acc, __nv_bfloat16* __restrict__ dq,
-                                  int64_t sb, int64_t ss, int64_t sh, const ChunkTable ct, int Hq,
-                                  int D, float scale, int64_t nslots) {
+// bf16 rows of the caller's layout.  A block takes 32 rows of a tile: its
+// warps read four columns of all 32 at a time (512 consecutive bytes) and
+// write whole rows, turned around in shared memory.  (A thread per eight
+// columns of a row read 16 bytes of each line: 17.7 instead of 12.7 us at
+// S = 4608, 24 heads, D = 128.)
+template <int D>
+__global__ void __launch_bounds__(256) dq_convert_kernel(const float* __restrict__ acc, __nv_bfloat16* __restrict__ dq,
+                                                         int64_t sb, int64_t ss, int64_t sh,
+                                                         const __grid_constant__ ChunkTable ct, int Hq, float scale) {
     griddep_wait();  // the previous kernel in the stream is complete (launch_kernel)
     griddep_launch_dependents();
-    const int g8 = D / 8;
-    const int64_t gt = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (gt >= nslots * g8) return;
-    const int64_t slot = gt / g8;
-    const int k8 = (int)(gt - slot * g8);
-    const int rr = (int)(slot % kTile);
-    const int64_t bht = slot / kTile;
-    const int t = (int)(bht % ct.ntiles);
-    const int64_t bh = bht / ct.ntiles;
-    const int h = (int)(bh % Hq), b = (int)(bh / Hq);
+    constexpr int ROWS = 32, C4 = D / 4, N = ROWS * C4 / 256;
+    __shared__ uint2 rows[ROWS][C4 + 1];  // four bf16 each; odd pitch, so that 16 rows of a column lie in all banks
+    const uint32_t bht = blockIdx.x / (kTile / ROWS), bh = bht / (uint32_t)ct.ntiles;
+    const int r0 = (int)(blockIdx.x % (kTile / ROWS)) * ROWS, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const float4* src = reinterpret_cast<const float4*>(acc + (int64_t)bht * kTile * D) + r0 + lane;
+    float4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = src[(warp + 8 * i) * kTile];
+    const int t = (int)(bht - bh * (uint32_t)ct.ntiles);
+    const int b = (int)(bh / (uint32_t)Hq), h = (int)(bh - (uint32_t)b * (uint32_t)Hq);
     const int c = chunk_of_tile(ct, t);
-    const int s = ct.off[c] + (t - ct.tile_off[c]) * kTile + rr;
-    if (s >= ct.off[c + 1]) return;
-    const float* tile = acc + bht * kTile * D;
-    const float4 lo = *reinterpret_cast<const float4*>(tile + ((int64_t)(2 * k8) * kTile + rr) * 4);
-    const float4 hi = *reinterpret_cast<const float4*>(tile + ((int64_t)(2 * k8 + 1) * kTile + rr) * 4);
-    uint4 v = make_uint4(pack_bf16x2(lo.x * scale, lo.y * scale), pack_bf16x2(lo.z * scale, lo.w * scale),
-                         pack_bf16x2(hi.x * scale, hi.y * scale), pack_bf16x2(hi.z * scale, hi.w * scale));
-    *reinterpret_cast<uint4*>(dq + b * sb + (int64_t)s * ss + h * sh + k8 * 8) = v;
+    const int s0 = ct.off[c] + (t - ct.tile_off[c]) * kTile + r0;
+    const int live = ct.off[c + 1] - s0;  // rows of the chunk from here on
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        rows[lane][warp + 8 * i] = make_uint2(pack_bf16x2(v[i].x * scale, v[i].y * scale), pack_bf16x2(v[i].z * scale, v[i].w * scale));
+    __syncthreads();
+    __nv_bfloat16* dst = dq + b * sb + (int64_t)s0 * ss + h * sh;
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const int e = i * 256 + (int)threadIdx.x, r = e / (D / 8), k8 = e % (D / 8);
+        const uint2 lo = rows[r][2 * k8], hi = rows[r][2 * k8 + 1];
+        if (r < live) *reinterpret_cast<uint4*>(dst + (int64_t)r * ss + k8 * 8) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
 }
 
 // Sum of the head-split partial dK / dV of the D = 256 backward:
@@ -766,7 +774,8 @@ int attn_fwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k
     p.debug = kernel_debug_bits();
     if (!p.status) return CTX_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    p.pdl = use_pdl(fwd_ctas(p.ct, (int)B, (int)Hq, (int)D), win ? window_tiles(p.win, p.ct.ntiles) : p.ct.ntiles, s);
+    p.pdl = use_pdl(fwd_ctas(p.ct, (int)B, (int)Hq, (int)D), win ? window_tiles(p.win, p.ct.ntiles) : p.ct.ntiles,
+                    kPdlSteps, s);
     if (log_enabled())
         fprintf(stderr,
                 "%s: B=%d S=%d Hq=%d Hkv=%d D=%d P=%d causal=%d%s order=%s partials=%d | %d query "
@@ -875,7 +884,9 @@ int attn_bwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k
     p.debug = kernel_debug_bits();
     if (!p.status) return CTX_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    p.pdl = D == 256 ? 0 : use_pdl(bwd_ctas, win ? window_tiles(p.win, p.ct.ntiles) : p.ct.ntiles, s);
+    p.pdl = win        ? use_pdl(bwd_ctas, window_tiles(p.win, p.ct.ntiles), kPdlStepsWindowBwd, s)
+            : D == 256 ? 0
+                       : use_pdl(bwd_ctas, p.ct.ntiles, kPdlSteps, s);
     if (log_enabled())
         fprintf(stderr,
                 "%s: B=%d S=%d Hq=%d Hkv=%d D=%d P=%d causal=%d%s | %d KV tiles, %lld CTAs (%s), "
@@ -886,13 +897,11 @@ int attn_bwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k
                 p.hsplit, p.head_major ? "head-major" : "tile-major");
     {
         // row statistics, and the fp32 dQ accumulator zeroed
-        const int64_t threads = (int64_t)slots * (D / 8);
-        const int blk = 256;
-        rc = launch_status(launch_kernel(p.pdl != 0, bwd_stats_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
-                                         dim3(blk), 0, s,
+        auto kern = D == 64 ? bwd_stats_kernel<64> : D == 128 ? bwd_stats_kernel<128> : bwd_stats_kernel<256>;
+        rc = launch_status(launch_kernel(p.pdl != 0, kern, dim3((unsigned)(slots * (D / 8) / 256)), dim3(256), 0, s,
             static_cast<const __nv_bfloat16*>(to.data), to.sb, to.ss, to.sh,
             static_cast<const __nv_bfloat16*>(tdo.data), tdo.sb, tdo.ss, tdo.sh, lse, nlse2_t,
-            delta_t, dq_acc, p.ct, (int)Hq, (int)S, (int)D, (int64_t)slots));
+            delta_t, dq_acc, p.ct, (int)Hq, (int)S));
         if (rc) return rc;
     }
     prof_record(1, 0, s);
@@ -916,12 +925,9 @@ int attn_bwd_call(const char* name, const ctx_tensor_t* q, const ctx_tensor_t* k
         if (rc) return rc;
     }
     {
-        const int64_t threads = (int64_t)slots * (D / 8);
-        const int blk = 256;
-        rc = launch_status(launch_kernel(p.pdl != 0, dq_convert_kernel, dim3((unsigned)((threads + blk - 1) / blk)),
-                                         dim3(blk), 0, s,
-            dq_acc, static_cast<__nv_bfloat16*>(tdq.data), tdq.sb, tdq.ss, tdq.sh, p.ct, (int)Hq,
-            (int)D, p.scale, (int64_t)slots));
+        auto kern = D == 64 ? dq_convert_kernel<64> : D == 128 ? dq_convert_kernel<128> : dq_convert_kernel<256>;
+        rc = launch_status(launch_kernel(p.pdl != 0, kern, dim3((unsigned)(slots / 32)), dim3(256), 0, s,
+            dq_acc, static_cast<__nv_bfloat16*>(tdq.data), tdq.sb, tdq.ss, tdq.sh, p.ct, (int)Hq, p.scale));
         if (rc) return rc;
     }
     return CTX_OK;

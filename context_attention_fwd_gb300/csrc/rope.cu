@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, kBlocks) norm_grad_kernel(con
     __shared__ float4 ws[4][32];  // twos 2q, 2q + 1 of group g at [q][g]
     __shared__ uint32_t partners[kStyle == kShifted ? kGradWarps : 1][kStyle == kShifted ? 32 * Partners<T>::kWords : 1];
     const Partners<T> pt{partners[kStyle == kShifted ? warp_id() : 0]};
+    griddep_launch_dependents();  // weight_grad_kernel, which waits for this kernel before it reads
     float2* cs = cs_all[warp_id()];
     const RowThread th(p, kStyle);
     const int per_pass = 32 >> p.log2_L;
@@ -611,6 +612,7 @@ template <typename T, int kMode>
 __global__ void __launch_bounds__(32 * kGradWarps) rope_pairs_kernel(const __grid_constant__ RopeParams p) {
     __shared__ float2 cs_all[kGradWarps][kMaxRopeDim / 2];
     __shared__ float sums[kMode == kNormGrad ? kGradWarps : 1][kMode == kNormGrad ? kMaxRopeDim : 1];
+    if constexpr (kMode == kNormGrad) griddep_launch_dependents();  // weight_grad_kernel
     float2* cs = cs_all[warp_id()];
     const int lane = lane_id(), np = p.D / 2;
     const int64_t units = (int64_t)p.B * p.S * p.units_per_token;
@@ -709,19 +711,24 @@ __global__ void __launch_bounds__(32 * kGradWarps) rope_pairs_kernel(const __gri
 }
 
 // dw = the sum of the blocks' partial gradients, in a fixed order: 32 columns
-// by 16 row groups per block.
-__global__ void weight_grad_kernel(const float* __restrict__ part, int blocks, int D, float* dwq, float* dwk) {
-    __shared__ float sm[16][33];
+// by 32 row groups per block.
+constexpr int kSumRows = 32;
+__global__ void __launch_bounds__(32 * kSumRows) weight_grad_kernel(const float* __restrict__ part, int blocks, int D,
+                                                                    float* dwq, float* dwk) {
+    griddep_wait();  // the gradient kernel is complete (launch_kernel)
+    __shared__ float sm[kSumRows][33];
     const int col = blockIdx.x * 32 + threadIdx.x;
     float v = 0.f;
-    if (col < 2 * D)
-        for (int i = threadIdx.y; i < blocks; i += 16) v += part[(int64_t)i * 2 * D + col];
+    if (col < 2 * D) {
+#pragma unroll 8
+        for (int i = threadIdx.y; i < blocks; i += kSumRows) v += part[(int64_t)i * 2 * D + col];
+    }
     sm[threadIdx.y][threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.y == 0 && col < 2 * D) {
         v = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v += sm[i][threadIdx.x];
+        for (int i = 0; i < kSumRows; ++i) v += sm[i][threadIdx.x];
         float* out = col < D ? dwq : dwk;
         if (out) out[col < D ? col : col - D] = v;
     }
@@ -887,9 +894,8 @@ int rope_call(const char* name, int mode, const ctx_tensor_t* const x[2], const 
     else e = launch_rope<kNormGrad>(p, (ctx_dtype_t)dtype, vec, (unsigned)grid, s);
     int rc = launch_status(e);
     if (rc || !want_dw) return rc;
-    weight_grad_kernel<<<(unsigned)((2 * D + 31) / 32), dim3(32, 16), 0, s>>>(p.dw_part, (int)grid, (int)D, p.dw[0],
-                                                                             p.dw[1]);
-    return launch_status();
+    return launch_status(launch_kernel(!stream_captured(s), weight_grad_kernel, dim3((unsigned)((2 * D + 31) / 32)),
+                                       dim3(32, kSumRows), 0, s, (const float*)p.dw_part, (int)grid, (int)D, p.dw[0], p.dw[1]));
 }
 
 }  // namespace
