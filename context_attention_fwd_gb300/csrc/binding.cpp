@@ -141,6 +141,7 @@ bool rope_of(PyObject* head, PyObject* turns, PyObject* positions, PyObject* off
     if (t.device() != dev) refuse("table: on ", t.device(), ", the tensors are on ", dev);
     if (!PyBytes_Check(head) || PyBytes_GET_SIZE(head) != (Py_ssize_t)sizeof(ctx_rope_t)) refuse("table: not a RopeTable");
     memcpy(r, PyBytes_AS_STRING(head), sizeof(ctx_rope_t));
+    r->turns = static_cast<const uint64_t*>(t.data_ptr());
     if (!given(positions)) {
         if (r->n_axes > 1) refuse("a table with several position axes needs positions");
         r->offset = PyLong_AsLongLong(offset);
