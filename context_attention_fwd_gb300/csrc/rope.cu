@@ -51,6 +51,7 @@ constexpr int kGradWarps = 4;  // warps of a norm-gradient block
 // which hold twice the words or angles, at 168 (fp32 at 128 spills: 183 us
 // instead of 125 on 10000 tokens of 24/24 heads, D = 128).
 constexpr int kGradBlocks = 4, kGradBlocksWide = 3;
+constexpr int kJoinedPasses = 4;  // up to which a rotation joins queries' and keys' heads (launch_rope_mode)
 constexpr int kMaxGradBlocks = 1024;  // blocks of the backward that leave partial weight gradients
 
 enum { kRotate = 0, kNorm = 1, kNormGrad = 2 };
@@ -76,6 +77,7 @@ struct RopeParams {
     int64_t pos_sb, pos_ss, pos_sa, offset;
     int n_axes, sec_end[4];     // pairs [sec_end[a-1], sec_end[a]) use axis a
     int interleaved;
+    int joined;                 // passes run over the queries' heads and then the keys' (passes[1] is 0)
     float m, sin_sign, eps;
     float* dw_part;             // [blocks][2][D], or null (a side without a tensor is not written)
     float* dw[2];
@@ -112,6 +114,24 @@ __device__ __forceinline__ T* token_row(const RopeRows& r, int b, int s) {
 // A warp's share of the work: one token (b, s) and a range of head passes.
 struct Unit {
     int b, s, part;
+};
+// A token's rows by head: one side's, or the queries' and then the keys'.
+template <typename T, bool kJoined>
+struct HeadRows {
+    T* row[kJoined ? 2 : 1];
+    int64_t sh[kJoined ? 2 : 1];
+    int first_k;
+    __device__ __forceinline__ HeadRows(const RopeParams& p, const RopeRows* r, int side, const Unit& u) {
+        first_k = p.H[0];
+#pragma unroll
+        for (int i = 0; i < (kJoined ? 2 : 1); ++i) {
+            row[i] = token_row<T>(r[side + i], u.b, u.s);
+            sh[i] = r[side + i].sh;
+        }
+    }
+    __device__ __forceinline__ T* at(int h) const {
+        return !kJoined || h < first_k ? row[0] + h * sh[0] : row[kJoined] + (h - first_k) * sh[kJoined];
+    }
 };
 __device__ __forceinline__ Unit unit_at(const RopeParams& p, int64_t u) {
     const int64_t token = u / p.units_per_token;
@@ -331,7 +351,7 @@ __device__ __forceinline__ float row_rsqrt(float v) {
 //   half         ya = a (wa c) + b (-wb s),  yb = b (wb c) + a (wa s)
 // in two-lane fp32 instructions.  kBatch passes are loaded before the first
 // is computed, so that a warp has kBatch kilobytes (16-bit types) in flight.
-template <typename T, int kStyle, bool kNormed, int kBatch, int kBlocks>
+template <typename T, int kStyle, bool kNormed, bool kJoined, int kBatch, int kBlocks>
 __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float2 cs_all[kWarps][kMaxRopeDim / 2];
     __shared__ uint32_t partners[kStyle == kShifted ? kWarps : 1][kStyle == kShifted ? 32 * Partners<T>::kWords : 1];
@@ -348,14 +368,12 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid
     // both sides in line where registers allow: their strides and pointers are
     // then constants of the launch, not indexed loads (133 -> 126 us, below)
 #pragma unroll(kNormed && kBatch > 2 ? 2 : 1)
-    for (int side = 0; side < 2; ++side) {
+    for (int side = 0; side < (kJoined ? 1 : 2); ++side) {
         const int base = side ? p.passes[0] : 0;
         const int p0 = max(first - base, 0), p1 = min(last - base, p.passes[side]);
         if (p0 >= p1) continue;
-        const T* xt = token_row<T>(p.x[side], u.b, u.s);
-        T* yt = token_row<T>(p.y[side], u.b, u.s);
-        const int64_t xh = p.x[side].sh, yh = p.y[side].sh;
-        const int H = p.H[side];
+        const int H = kJoined ? p.H[0] + p.H[1] : p.H[side];
+        const HeadRows<T, kJoined> xt(p, p.x, side, u), yt(p, p.y, side, u);
         float2 k[16];
         bool have_k = false;
 #pragma unroll 1
@@ -363,7 +381,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid
             Group<T> raw[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
-                if (ps + i < p1) raw[i].load(xt + min((ps + i) * per_pass + th.slot, H - 1) * xh, th.at);
+                if (ps + i < p1) raw[i].load(xt.at(min((ps + i) * per_pass + th.slot, H - 1)), th.at);
             if (!have_angles) {
                 token_angles<true, sizeof(T) == 4>(p, u, cs);
                 have_angles = true;
@@ -441,7 +459,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) rope_kernel(const __grid
                         y.set(4 + j, vb);
                     }
                 }
-                if (h < H && th.live) y.store(yt + h * yh, th.at);
+                if (h < H && th.live) y.store(yt.at(h), th.at);
             }
         }
     }
@@ -775,12 +793,19 @@ cudaError_t launch_rope_mode(const RopeParams& p, bool vec, unsigned grid, cudaS
         constexpr bool kNormed = kMode == kNorm;
         constexpr int kLong = sizeof(T) == 4 ? 2 : kNormed ? 6 : 3, kLongBlocks = kNormed ? 8 : 12;
         constexpr int kShort = 2, kShortBlocks = 12;
-        const bool few = kNormed && std::max(p.passes[0], p.passes[1]) <= 3;
-        auto kern = style == kInter ? (few ? rope_kernel<T, kInter, kNormed, kShort, kShortBlocks>
-                                           : rope_kernel<T, kInter, kNormed, kLong, kLongBlocks>)
-                    : style == kHalf ? (few ? rope_kernel<T, kHalf, kNormed, kShort, kShortBlocks>
-                                            : rope_kernel<T, kHalf, kNormed, kLong, kLongBlocks>)
-                                     : rope_kernel<T, kShifted, kNormed, kShort, 8>;
+        //
+        // The rotation's passes run over queries' and keys' heads together where
+        // that makes fewer of them (20000 tokens of 6/2 heads, D = 128: 18 us, a
+        // side at a time 23), and with 16-bit types where they are few, as the
+        // factors are then folded once (272440 of 8/2, D = 80: 268 and 288; 30000
+        // of 8/8: 41.9 and 43.3; but 20000 of 24/8, eight passes: 53.2 and 51.2,
+        // and of 8/8 in fp32 55.5 and 51.7).
+        const bool few = kNormed ? std::max(p.passes[0], p.passes[1]) <= 3 : p.joined != 0;
+        auto kern = style == kInter ? (few ? rope_kernel<T, kInter, kNormed, !kNormed, kShort, kShortBlocks>
+                                           : rope_kernel<T, kInter, kNormed, false, kLong, kLongBlocks>)
+                    : style == kHalf ? (few ? rope_kernel<T, kHalf, kNormed, !kNormed, kShort, kShortBlocks>
+                                            : rope_kernel<T, kHalf, kNormed, false, kLong, kLongBlocks>)
+                                     : rope_kernel<T, kShifted, kNormed, !kNormed, kShort, 8>;
         return launch_kernel(false, kern, dim3(grid), blk, 0, s, p);
     }
 }
@@ -881,6 +906,14 @@ int rope_call(const char* name, int mode, const ctx_tensor_t* const x[2], const 
     p.L = 1 << p.log2_L;
     const int per_pass = 32 / p.L;
     for (int i = 0; i < 2; ++i) p.passes[i] = (p.H[i] + per_pass - 1) / per_pass;
+    const int together = (p.H[0] + p.H[1] + per_pass - 1) / per_pass;
+    const bool shifted = !p.interleaved && p.rot % 16 != 0;
+    if (mode == kRotate && vec &&
+        (shifted || together < p.passes[0] + p.passes[1] || (size == 2 && together <= kJoinedPasses))) {
+        p.joined = 1;
+        p.passes[0] = together;
+        p.passes[1] = 0;
+    }
     const int total = p.passes[0] + p.passes[1];
     const int64_t tokens = B * S;
     const int sms = num_sms();
@@ -894,7 +927,7 @@ int rope_call(const char* name, int mode, const ctx_tensor_t* const x[2], const 
     const bool walk = mode == kNormGrad || !vec;  // kernels whose warps walk many units
     const int warps = walk ? kGradWarps : kWarps;
     int64_t grid = (units + warps - 1) / warps;
-    const bool wide = size == 4 || (!p.interleaved && p.rot % 16 != 0);
+    const bool wide = size == 4 || shifted;
     const int64_t per_sm = !vec ? 16 : wide ? kGradBlocksWide : kGradBlocks;
     if (walk) grid = std::min<int64_t>(grid, std::min<int64_t>(per_sm * sms, kMaxGradBlocks));
     if (grid > INT32_MAX) return CTX_ERR_INVALID_ARG;

@@ -112,6 +112,23 @@ def test_rotation_and_its_gradient(B, S, Hq, Hk, D, rot, inter, dt, layout, pos)
                   2.0 ** -20 * 1.25 * _pair_len(x64, rot, inter), dt)
 
 
+@pytest.mark.parametrize("D,rot", [(64, 64), (80, 32), (128, 36), (256, 128)])
+@pytest.mark.parametrize("Hq,Hk,S,inter,dt", [
+    (3, 1, 300, False, BF), (8, 2, 3000, True, BF), (6, 2, 7, False, F32), (1, 1, 3000, True, FP), (5, 3, 200, True, F32),
+    (2, 9, 3000, False, FP), (8, 8, 300, False, BF)])
+def test_few_heads_of_both_sides(Hq, Hk, S, inter, dt, D, rot):
+    """Queries' and keys' heads that share a pass, stored differently."""
+    test_rotation_and_its_gradient(2, S, Hq, Hk, D, rot, inter, dt, "bshd", "each")
+    g = torch.Generator().manual_seed(S)
+    table = ctx.rope_table(rot, interleaved=inter)
+    q, k = _rand(g, 2, S, Hq, D, dt), _rand(g, 2, S, Hk + 2, D, dt, "sbhd")[:, :, 1:-1]
+    a, b = ctx.rope_fwd(q, k, table, offset=5)
+    assert torch.equal(a, ctx.rope_fwd(q, None, table, offset=5)[0])
+    assert torch.equal(b, ctx.rope_fwd(k, None, table, offset=5)[0])
+    ctx.rope_fwd(q, k, table, offset=5, q_out=q, k_out=k)
+    assert torch.equal(q, a) and torch.equal(k, b)
+
+
 @pytest.mark.parametrize("wdt", [None, torch.float32, "same"])
 @pytest.mark.parametrize("B,S,Hq,Hk,D,rot,inter,dt,layout,pos", CASES)
 def test_norm_and_its_gradient(B, S, Hq, Hk, D, rot, inter, dt, layout, pos, wdt):
